@@ -93,13 +93,16 @@ enum idx_status_code {
   IDX_ERR_DEVICE = -7,      /* idx_status: a kernel set the device error word */
   IDX_ERR_CUDA = -8,        /* idx_status: the stream itself reported a CUDA error */
   IDX_ERR_UNSUPPORTED = -9, /* no device code for this GPU (not sm_100) */
-  IDX_ERR_SCRATCH = -10     /* the scratch is too small: idx_score_topk_noalloc's fixed scratch, idx_project's ws */
+  IDX_ERR_SCRATCH = -10     /* the scratch is too small: idx_score_topk_noalloc's fixed scratch, idx_project's and
+                               idx_tree_mla's ws */
 };
 
 /* Bits of the device error word (returned by idx_device_error_bits). */
 #define IDX_DEV_ERR_TIMEOUT 0x1u  /* a bounded wait inside a kernel gave up */
 #define IDX_DEV_ERR_POSITION 0x2u /* idx_quant_append: positions[b] < 0 or positions[b] + n > T_cap */
-#define IDX_DEV_ERR_LENGTH 0x4u   /* score/top-k: lengths[b] < n or lengths[b] > max_len */
+#define IDX_DEV_ERR_LENGTH 0x4u   /* score/top-k: lengths[b] < n or lengths[b] > max_len; the paged calls: a count or
+                                     a length out of range */
+#define IDX_DEV_ERR_PAGE 0x8u     /* the paged calls: a page number outside [0, num_pages) */
 
 /*
  * idx_quant — "Hadamard rotation" page (rotation equation) followed by the
@@ -347,6 +350,94 @@ IDX_API int idx_merge_topk(const idx_cand_t* cand, int G, int64_t rows, int kin,
  */
 IDX_API int idx_sparse_mla_decode(const uint16_t* q, const uint16_t* kv, const int32_t* indices, int B, int H,
                                   int64_t T_cap, int k, float softmax_scale, float* out, idx_stream_t stream);
+
+/*
+ * The paged latent cache: cache [num_pages, page_size, 576] bf16, one row per
+ * position (512 latent features, then the 64 rotated ones).  Position t of
+ * sequence b is row t mod page_size of page page_table[b, t / page_size]
+ * (page_table [B, max_pages] int32; entries past a sequence's last position are
+ * not read).  page_size is any number ≥ 1; sequences may share pages that
+ * neither of them writes.  num_pages · page_size < 2^31, max_pages · page_size < 2^31.
+ *
+ * idx_latent_append — the new tokens' rows: the latent's RMSNorm, the rotation
+ * of the shared rotary key, and the write into the paged cache; and, in the
+ * same launch, the rotation of the queries' rotary part into the joined queries
+ * that idx_tree_mla reads.
+ *   kv_proj  [B, n, 576] bf16: the latent and the rotary key as projected, in
+ *            rows kv_tok_pitch elements apart, sequences kv_seq_pitch apart (the
+ *            tail of a wider projection is read in place); 16-byte aligned,
+ *            pitches multiples of 8.
+ *   gain     [512] fp32, eps ≥ 0: latent[j] = bf16(x[j] · (Σx²/512 + eps)^-1/2 · gain[j]).
+ *   rope_cos, rope_sin [B, n, 32] fp32 of each token's position (for a tree of
+ *            drafts its depth after the context, not its slot).  interleaved = 1:
+ *            features 2i and 2i + 1 are the pair turned by θ_i; 0: features i and
+ *            i + 32.
+ *   positions [B] int32: slot of each sequence's first new token; token i goes
+ *            to slot positions[b] + i.
+ *   counts   [B] int32 or NULL (all n): sequence b has counts[b] ≤ n new tokens;
+ *            nothing is read, written or checked for the rows behind them.
+ *   q_pe     [B, n, H, 64] bf16 or NULL (H = 0), with pitches in elements as
+ *            kv_proj's; q_out [B, n, H, 576] bf16: features 512 … 575 are written,
+ *            the first 512 (the absorbed content query) are left alone.
+ * fp32 arithmetic, one rounding to bf16 per output.  All pointers but positions,
+ * counts and page_table are 16-byte aligned.  A sequence whose slots are
+ * negative or pass max_pages · page_size raises IDX_DEV_ERR_POSITION and one
+ * with counts[b] outside [0, n] IDX_DEV_ERR_LENGTH: neither writes anything (its
+ * queries included).  A token whose page number is outside [0, num_pages)
+ * raises IDX_DEV_ERR_PAGE and its cache row is not written.  Two tokens of a call
+ * that share a slot leave one of their rows there, which one is not specified.
+ */
+IDX_API int idx_latent_append(const uint16_t* kv_proj, int64_t kv_seq_pitch, int64_t kv_tok_pitch, const float* gain,
+                              float eps, const float* rope_cos, const float* rope_sin, int interleaved,
+                              const int32_t* positions, const int32_t* counts, const int32_t* page_table,
+                              int max_pages, int B, int n, uint16_t* cache, int num_pages, int page_size,
+                              const uint16_t* q_pe, int64_t q_seq_pitch, int64_t q_tok_pitch, int64_t q_head_pitch,
+                              int H, uint16_t* q_out, idx_stream_t stream);
+
+/* Element type of idx_tree_mla's out. */
+enum idx_out_dtype { IDX_OUT_F32 = 0, IDX_OUT_BF16 = 1 };
+#define IDX_MAX_DRAFTS 64 /* rows per sequence of idx_tree_mla: the bits of a tree mask */
+
+/*
+ * idx_tree_mla — latent attention of each sequence's last rows over its paged
+ * cache: a tree of drafted tokens (speculative decoding), a chain of new tokens,
+ * or one decode token (n = 1); over the whole context, or over the positions
+ * that the indexer selected for each row.  The rows' own cache rows are appended
+ * first (idx_latent_append).
+ *   q        [B, n, H, 576] bf16, 1 ≤ n ≤ IDX_MAX_DRAFTS, H ≥ 1.
+ *   lengths  [B] int32: cached positions including the drafts; counts [B] int32
+ *            or NULL (all n).  Row i < counts[b] is draft i, at slot ctx + i with
+ *            ctx = lengths[b] − counts[b].  Outputs of rows behind counts[b] are
+ *            left as they were.
+ *   max_len  host bound: lengths[b] ≤ max_len ≤ max_pages · page_size.
+ *   tree_mask [B, n] uint64 or NULL (a chain: row i sees drafts 0 … i): row i
+ *            sees draft j < counts[b] iff bit j of tree_mask[b, i] is set.
+ *   indices  [B, n, k] int32 or NULL (the whole context, k = 0): the context
+ *            positions row i attends to, in any order, as idx_score_topk gives
+ *            them; entries outside [0, ctx) select nothing, a position named
+ *            twice counts twice.  The drafts are seen as by tree_mask either way.
+ *   s[t] = softmax_scale · Σ_d q[d] · row_t[d];  p = softmax of s over the row's positions
+ *   out      [B, n, H, 512] of out_dtype: Σ_t p[t] · row_t[0:512].
+ *   lse      [B, n, H] fp32 or NULL: ln Σ_t exp(s[t]) (joins results over other keys).
+ *   A row that sees nothing gives out = 0, lse = −inf.  Cache rows that a
+ *   sequence does not hold are never read as numbers.
+ *   ws / ws_bytes: at least idx_tree_mla_workspace_size(B, n, H, max_len, k)
+ *            bytes, 16-byte aligned (may be NULL where that is 0).  It holds
+ *            partial results inside the call: calls (or captured graphs) that may
+ *            run at the same time need one each.
+ * q, cache, out, ws: 16-byte aligned; tree_mask 8.  Scores and sums in fp32.
+ * Errors: IDX_ERR_SHAPE, IDX_ERR_NULL, IDX_ERR_ALIGN, IDX_ERR_FMT (out_dtype),
+ * IDX_ERR_SCRATCH.  counts[b] outside [0, n], lengths[b] < counts[b] or
+ * lengths[b] > max_len raise IDX_DEV_ERR_LENGTH and leave the sequence's outputs as
+ * they were; a page number outside [0, num_pages) raises IDX_DEV_ERR_PAGE and its
+ * positions are not seen.
+ */
+IDX_API size_t idx_tree_mla_workspace_size(int B, int n, int H, int max_len, int k);
+IDX_API int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int32_t* page_table, int max_pages,
+                         int num_pages, int page_size, const int32_t* lengths, const int32_t* counts, int B, int n,
+                         int H, int max_len, const uint64_t* tree_mask, const int32_t* indices, int k,
+                         float softmax_scale, void* out, int out_dtype, float* lse, void* ws, size_t ws_bytes,
+                         idx_stream_t stream);
 
 /*
  * idx_score_topk — scores and top-k in one call, arguments as in idx_score /

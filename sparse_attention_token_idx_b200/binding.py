@@ -23,8 +23,14 @@ DIM = 128
 DEV_ERR_TIMEOUT = 0x1
 DEV_ERR_POSITION = 0x2
 DEV_ERR_LENGTH = 0x4
+DEV_ERR_PAGE = 0x8
 SCALE_F32 = 0
 SCALE_E8M0 = 1
+OUT_F32 = 0
+OUT_BF16 = 1
+MAX_DRAFTS = 64
+LATENT = 512                                # latent features of a cache row, then ROTARY rotated ones
+ROTARY = 64
 SCORE_F32 = 0
 SCORE_BF16 = 1
 MASK_BOUND_BF16 = -3.3895313892515355e38    # most negative finite bfloat16
@@ -50,6 +56,11 @@ SIGNATURES = {
     "idx_gather_scores": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _P, _P]),
     "idx_merge_topk": (_I, [_P, _I, _I64, _I, _I, _P, _P]),
     "idx_sparse_mla_decode": (_I, [_P, _P, _P, _I, _I, _I64, _I, ctypes.c_float, _P, _P]),
+    "idx_latent_append": (_I, [_P, _I64, _I64, _P, ctypes.c_float, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P, _I, _I, _P,
+                               _I64, _I64, _I64, _I, _P, _P]),
+    "idx_tree_mla": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _I, _P, _P, _I, ctypes.c_float, _P, _I, _P, _P,
+                          _SZ, _P]),
+    "idx_tree_mla_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "idx_score_topk": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "idx_score_topk_noalloc": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
     "idx_score_topk_ex": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
@@ -339,6 +350,140 @@ def sparse_mla_decode(q, kv, indices, softmax_scale: float, out=None, stream=Non
                                         B, H, kv.shape[1], indices.shape[1], float(softmax_scale),
                                         _ptr(out, torch.float32, "out"), _stream(stream)), "idx_sparse_mla_decode")
     return out
+
+
+def _same_device(what: str, **tensors):
+    """The one CUDA device that all the tensors (None: absent) are on."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise IdxError(f"{what}: {name} must be a CUDA tensor")
+        if dev is not None and t.device != dev:
+            raise IdxError(f"{what}: {name} is on {t.device}, other arguments on {dev}")
+        dev = t.device
+    return dev
+
+
+def _typed(what: str, name: str, t, dtype, shape):
+    if t is None:
+        return
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise IdxError(f"{what}: {name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: {name} has shape {list(t.shape)}, expected {list(shape)}")
+
+
+def _pitches(what: str, name: str, t):
+    """Element pitches of all dimensions but the last, which must be contiguous;
+    a dimension of one entry has no pitch (0)."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise IdxError(f"{what}: {name}'s last dimension must be contiguous")
+    return [0 if t.shape[d] <= 1 else t.stride(d) for d in range(t.dim() - 1)]
+
+
+def latent_append(kv_proj, gain, eps: float, rope_cos, rope_sin, positions, page_table, cache, *,
+                  interleaved: bool = True, counts=None, q_pe=None, q_out=None, stream=None):
+    """New tokens' rows into the paged latent cache: kv_proj [B, n, 576] bf16 (any
+    pitch that is a multiple of 8 elements: the tail of a wider projection) gets
+    the RMSNorm of its 512 latent features (gain [512] fp32) and the rotation of
+    its 64 rotary ones (tables [B, n, 32] fp32) and goes to slots positions[b] …
+    of cache [num_pages, page_size, 576] bf16 through page_table [B, max_pages]
+    int32.  counts [B] int32: new tokens per sequence (None: n each).  With q_pe
+    [B, n, H, 64] bf16 (strided likewise), its rotation is written to features
+    512 … 575 of q_out [B, n, H, 576] bf16 (allocated when None; its other
+    features are then unset).  Returns q_out."""
+    what = "latent_append"
+    if kv_proj.dim() != 3 or cache.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("latent_append: kv_proj [B, n, 576], cache [num_pages, page_size, 576], "
+                         "page_table [B, max_pages]")
+    B, n = kv_proj.shape[:2]
+    row = LATENT + ROTARY
+    H = 0
+    if q_pe is not None:
+        if q_pe.dim() != 4:
+            raise ValueError("latent_append: q_pe [B, n, H, 64]")
+        H = q_pe.shape[2]
+    elif q_out is not None:
+        raise ValueError("latent_append: q_out without q_pe")
+    for name, t, dtype, shape in (
+            ("kv_proj", kv_proj, _BF16, (B, n, row)), ("gain", gain, torch.float32, (LATENT,)),
+            ("rope_cos", rope_cos, torch.float32, (B, n, ROTARY // 2)),
+            ("rope_sin", rope_sin, torch.float32, (B, n, ROTARY // 2)), ("positions", positions, torch.int32, (B,)),
+            ("counts", counts, torch.int32, (B,)), ("page_table", page_table, torch.int32, (B, page_table.shape[1])),
+            ("cache", cache, _BF16, (cache.shape[0], cache.shape[1], row)),
+            ("q_pe", q_pe, _BF16, (B, n, H, ROTARY)), ("q_out", q_out, _BF16, (B, n, H, row))):
+        _typed(what, name, t, dtype, shape)
+    dev = _same_device(what, kv_proj=kv_proj, gain=gain, rope_cos=rope_cos, rope_sin=rope_sin, positions=positions,
+                       counts=counts, page_table=page_table, cache=cache, q_pe=q_pe, q_out=q_out)
+    kb, kt = _pitches(what, "kv_proj", kv_proj)
+    qb, qt, qh = _pitches(what, "q_pe", q_pe) if q_pe is not None else (0, 0, 0)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if q_pe is not None and q_out is None:
+            q_out = torch.empty((B, n, H, row), dtype=torch.bfloat16, device=dev)
+        _check(load().idx_latent_append(
+            kv_proj.data_ptr(), kb, kt, _ptr(gain, name="gain"), float(eps), _ptr(rope_cos, name="rope_cos"),
+            _ptr(rope_sin, name="rope_sin"), int(bool(interleaved)), _ptr(positions, name="positions"),
+            _ptr(counts, name="counts"), _ptr(page_table, name="page_table"), page_table.shape[1], B, n,
+            _ptr(cache, name="cache"), cache.shape[0], cache.shape[1], q_pe.data_ptr() if H else None, qb, qt, qh, H,
+            _ptr(q_out, name="q_out") if H else None, _stream(stream)), "idx_latent_append")
+    return q_out
+
+
+def tree_mla_workspace_size(B: int, n: int, H: int, max_len: int, k: int = 0) -> int:
+    return int(load().idx_tree_mla_workspace_size(B, n, H, max_len, k))
+
+
+def tree_mla(q, cache, page_table, lengths, softmax_scale: float, *, max_len: int, counts=None, tree_mask=None,
+             indices=None, out=None, lse=None, ws=None, stream=None):
+    """Latent attention of each sequence's last rows (drafted tokens, whose cache
+    rows are appended) over its paged cache: q [B, n, H, 576] bf16, cache
+    [num_pages, page_size, 576] bf16, page_table [B, max_pages], lengths [B] int32
+    (drafts included) → (out [B, n, H, 512], lse [B, n, H] fp32 natural log).
+    counts [B] int32: drafts per sequence (None: n each); rows behind them are left
+    as they were.  tree_mask [B, n] int64: bit j of row i set where it sees draft j
+    (None: a chain).  indices [B, n, k] int32: the context positions each row
+    attends to (None: the whole context).  out bf16 or fp32 (allocated as bf16 when
+    None, its rows behind the counts unset), ws: uint8 workspace of
+    tree_mla_workspace_size bytes (allocated on the stream when None)."""
+    what = "tree_mla"
+    if q.dim() != 4 or cache.dim() != 3 or page_table.dim() != 2 or (indices is not None and indices.dim() != 3):
+        raise ValueError("tree_mla: q [B, n, H, 576], cache [num_pages, page_size, 576], page_table [B, max_pages], "
+                         "indices [B, n, k]")
+    B, n, H = q.shape[:3]
+    row = LATENT + ROTARY
+    if n > MAX_DRAFTS:
+        raise ValueError(f"tree_mla: at most {MAX_DRAFTS} rows per sequence")
+    k = indices.shape[2] if indices is not None else 0
+    if indices is not None and k == 0:
+        raise ValueError("tree_mla: indices of width 0 (pass None for the whole context)")
+    for name, t, dtype, shape in (
+            ("q", q, _BF16, (B, n, H, row)), ("cache", cache, _BF16, (cache.shape[0], cache.shape[1], row)),
+            ("page_table", page_table, torch.int32, (B, page_table.shape[1])), ("lengths", lengths, torch.int32, (B,)),
+            ("counts", counts, torch.int32, (B,)), ("tree_mask", tree_mask, (torch.int64, torch.uint64), (B, n)),
+            ("indices", indices, torch.int32, (B, n, k)),
+            ("out", out, (torch.bfloat16, torch.float32), (B, n, H, LATENT)),
+            ("lse", lse, torch.float32, (B, n, H))):
+        _typed(what, name, t, dtype, shape)
+    dev = _same_device(what, q=q, cache=cache, page_table=page_table, lengths=lengths, counts=counts,
+                       tree_mask=tree_mask, indices=indices, out=out, lse=lse, ws=ws)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):     # what is allocated here belongs to the call's stream
+        if out is None:
+            out = torch.empty((B, n, H, LATENT), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((B, n, H), dtype=torch.float32, device=dev)
+        if ws is None:
+            need = tree_mla_workspace_size(B, n, H, max_len, k)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(load().idx_tree_mla(
+            _ptr(q, name="q"), _ptr(cache, name="cache"), _ptr(page_table, name="page_table"), page_table.shape[1],
+            cache.shape[0], cache.shape[1], _ptr(lengths, name="lengths"), _ptr(counts, name="counts"), B, n, H,
+            max_len, _ptr(tree_mask, name="tree_mask"), _ptr(indices, name="indices") if k else None, k,
+            float(softmax_scale), _ptr(out, name="out"), OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32,
+            _ptr(lse, name="lse"), _ptr(ws, name="ws"), 0 if ws is None else ws.numel() * ws.element_size(),
+            _stream(stream)), "idx_tree_mla")
+    return out, lse
 
 
 def topk(scores, lengths, causal: bool, k: int, max_len: int, out=None, stream=None):
