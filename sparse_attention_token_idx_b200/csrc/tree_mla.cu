@@ -21,7 +21,7 @@
 // share's end leaves partial (O, max, sums) in the workspace; a second kernel
 // joins them in a fixed order.
 //
-// One CTA, 10 warps:
+// One CTA, 12 warps (20 for N = 64):
 //   warp 0     walks the share: publishes each piece (item, tile range, row masks),
 //              loads its queries, and streams the tiles' rows by TMA — boxes of
 //              whole page runs for dense tiles, tile::gather4 by row number for
@@ -29,7 +29,8 @@
 //              number −1 and arrives as zeros (never as what memory holds);
 //   warp 1     issues the MMAs: scores of tile t, then its product, so that tile
 //              t + 1 streams into the parts of the buffer that the product has freed;
-//   warps 2-9  softmax: thread ↔ (key, half of the rows); the column maxima by a
+//   warps 2, 3 issue two thirds of the copies (a selection's tile is 288 of them);
+//   warps 4 …  softmax: thread ↔ (key, part of the rows); the column maxima by a
 //              transposing butterfly across lanes and shared memory across warps; a
 //              running reference maximum per row, raised only when a tile passes it by
 //              2^8 (then O in TMEM is rescaled); P = 2^(s − m) in bf16 for the tensor
@@ -51,17 +52,21 @@ namespace {
 
 constexpr int kLat = 512, kRow = 576;
 constexpr int kTile = 128;                    // keys per tile
-constexpr int kThreads = 320;
 constexpr int kPair = 32768;                  // 128 keys × 128 latent features: two 64-feature chunks
 constexpr int kChunk = 16384;                 // 128 keys × 64 features
 constexpr int kMaxTeam = 16;
 constexpr int kMinShare = 2;                  // tiles per team below which work is not split further
+constexpr int kCopyWarps = 4;                 // warps that copy the tiles
+constexpr int kFirstSoft = 2 + kCopyWarps;    // planner, MMA issuer, copies, then the softmax
 constexpr float kRaise = 8.f;                 // log2 margin of the reference maximum
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int N>
 struct Cfg {
-  static constexpr int kNC = N / 2;                         // rows per softmax thread
+  static constexpr int kSoftWarps = N == 64 ? 16 : 8;
+  static constexpr int kParts = kSoftWarps / 4;             // row parts, each of four warps (128 keys)
+  static constexpr int kNC = N / kParts;                    // rows per softmax thread
+  static constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
   static constexpr int kPairs = N == 16 ? 5 : 4;            // latent buffers
   static constexpr int kRopes = N == 32 ? 2 : 1;            // rotary-chunk buffers
   static constexpr bool kAliasP = N == 64;                  // P takes the rotary chunk's place after the scores
@@ -89,24 +94,29 @@ struct Cut {                                  // an item that begins in a share 
 template <int N>
 struct Misc {
   uint64_t mask[2][N];                        // per piece parity: drafts each column sees
-  float wmax[2][2][4][32];                    // per tile parity, row half, warp: column maxima
-  float m[8][32], alpha[8][32];               // per softmax warp
-  float sum[2][2][4][32];                     // sum kind, row half, warp
+  float wmax[2][Cfg<N>::kParts][4][Cfg<N>::kNC];   // per tile parity, row part, warp: column maxima
+  float m[Cfg<N>::kSoftWarps][Cfg<N>::kNC], alpha[Cfg<N>::kSoftWarps][Cfg<N>::kNC];
+  float sum[Cfg<N>::kParts][4][Cfg<N>::kNC];  // row part, warp
   alignas(16) uint8_t kind[2][kTile];         // per tile parity and key: 0 unseen, 1 context, 2 + j draft j
+  alignas(16) int row[2][kTile];              // per tile parity: cache rows of the keys, −1: none
+  int last[2];                                // per tile parity: no tile, the list has ended
   Piece piece[2];
-  long long scan[kThreads / 32];
+  long long scan[Cfg<N>::kThreads / 32];
   long long start_off, total;
   int start_b;
   uint64_t pair_full[5], pair_empty[5], rope_full[2], rope_empty[2];
   uint64_t q_full, q_empty, s_full, p_full, o_full, o_free, drain;
-  uint64_t kind_full[2], piece_full[2], piece_empty[2];
+  uint64_t tile_full[2], tile_read[2], piece_full[2], piece_empty[2];
   uint32_t tmem;
   int abort_flag;
 };
 
 struct TreeParams {
   const int32_t* table;
-  int max_pages, num_pages, page_size, box_rows;   // box_rows 0: no boxes
+  const uint16_t* cache;
+  int max_pages, num_pages, page_size;
+  uint32_t div_mul;                           // x / page_size = x · div_mul >> div_shift for x < 2^31
+  int div_shift;
   const int32_t *lengths, *counts;
   int B, n, H, max_len;
   const uint64_t* mask;
@@ -118,7 +128,7 @@ struct TreeParams {
   float* lse;
   int team, blocks;                           // CTAs per team, row blocks (of `team` groups) per token set
   int teams, whole;                           // whole: items are not cut
-  float* part;                                // [CTA][2] partial slots of N·(512 + 3) floats
+  float* part;                                // [CTA][2] partial slots of N·(512 + 2) floats
   Cut* cuts;                                  // [CTA]
   unsigned long long budget_ns;
   unsigned int* err;
@@ -130,13 +140,28 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
   return p != 0;
 }
-// four rows of a [rows, 576] array, 64 features from x; a row number outside the array reads zeros
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int r0, int r1,
-                                            int r2, int r3) {
+// mbar_wait that polls 256 times before it looks at the clock: a read of the
+// global timer takes about 1 000 cycles, which every wait that does not succeed
+// at once would add to its hand-off
+__device__ __forceinline__ bool mbar_wait_polling(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
+                                                  volatile int* abort_flag, unsigned int* err) {
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, budget_ns, abort_flag, err);
+}
+// 16 bytes into shared memory, zeros where bytes = 0; cp_async_arrive makes the
+// barrier count this thread once its copies so far have landed
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
-      "%6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -172,8 +197,8 @@ __device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void bar_half(int half) {            // the 128 softmax threads of a row half
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+__device__ __forceinline__ void bar_part(int part) {            // the 128 softmax threads of a row part
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
 }
 
 // NC consecutive 32-bit columns of this warp's 32 lanes
@@ -193,10 +218,6 @@ __device__ __forceinline__ void tmem_ld<16>(uint32_t a, uint32_t* r) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(a));
 }
-template <>
-__device__ __forceinline__ void tmem_ld<32>(uint32_t a, uint32_t* r) {
-  tmem_ld32_nowait(a, r);
-}
 template <int NC>
 __device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t* r);
 template <>
@@ -209,11 +230,6 @@ template <>
 __device__ __forceinline__ void tmem_st<16>(uint32_t a, const uint32_t* r) {
   tmem_st<8>(a, r);
   tmem_st<8>(a + 8, r + 8);
-}
-template <>
-__device__ __forceinline__ void tmem_st<32>(uint32_t a, const uint32_t* r) {
-  tmem_st<16>(a, r);
-  tmem_st<16>(a + 16, r + 16);
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // ties loaded registers to a point after tmem_wait()
@@ -277,11 +293,10 @@ __device__ __forceinline__ uint64_t draft_mask(const TreeParams& p, int b, int i
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 1)
-    tree_mla_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_row,
-                    const __grid_constant__ CUtensorMap tmap_box, const TreeParams p) {
+__global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
+    tree_mla_kernel(const __grid_constant__ CUtensorMap tmap_q, const TreeParams p) {
   using C = Cfg<N>;
-  constexpr int NC = C::kNC;
+  constexpr int NC = C::kNC, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc<N>& ms = *reinterpret_cast<Misc<N>*>(smem + C::kOffMisc);
@@ -292,32 +307,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kPairs; ++i) {
-      mbar_init(&ms.pair_full[i], 1);
+      mbar_init(&ms.pair_full[i], kCopyWarps * 32);
       mbar_init(&ms.pair_empty[i], 1);
     }
     for (int i = 0; i < C::kRopes; ++i) {
-      mbar_init(&ms.rope_full[i], 1);
+      mbar_init(&ms.rope_full[i], kCopyWarps * 32);
       mbar_init(&ms.rope_empty[i], 1);
     }
     mbar_init(&ms.q_full, 1);
     mbar_init(&ms.q_empty, 1);
     mbar_init(&ms.s_full, 1);
-    mbar_init(&ms.p_full, 8);
+    mbar_init(&ms.p_full, C::kSoftWarps);
     mbar_init(&ms.o_full, 1);
-    mbar_init(&ms.o_free, 8);
+    mbar_init(&ms.o_free, C::kSoftWarps);
     mbar_init(&ms.drain, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms.kind_full[i], 1);
+      mbar_init(&ms.tile_full[i], 1);
+      mbar_init(&ms.tile_read[i], kCopyWarps + C::kSoftWarps);
       mbar_init(&ms.piece_full[i], 1);
-      mbar_init(&ms.piece_empty[i], 9);
+      mbar_init(&ms.piece_empty[i], C::kSoftWarps + 1);
     }
     ms.abort_flag = 0;
     ms.start_b = p.B;
     ms.start_off = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
-    tma_prefetch_desc(&tmap_row);
-    tma_prefetch_desc(&tmap_box);
   }
   if (warp == 1) tmem_alloc(&ms.tmem, C::kTmemCols);
 
@@ -362,11 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const uint32_t tmem = ms.tmem;
   const uint32_t smem_base = smem_u32(smem);
-
   if (warp == 0) {
-    // ================================================================ loader
+    // ================================================================ planner
     bool ok = true;
-    int pairs = 0, ropes = 0, tiles = 0, pieces = 0;       // running counts
+    int tiles = 0, pieces = 0;                             // running counts
     long long cur = begin;
     int b = ms.start_b;
     long long off = ms.start_off;
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // waits of the whole warp: lane 0 polls
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       int w = 1;
-      if (lane == 0) w = mbar_wait_sleep(bar, parity, budget, abort_flag, p.err) ? 1 : 0;
+      if (lane == 0) w = mbar_wait_polling(bar, parity, budget, abort_flag, p.err) ? 1 : 0;
       w = __shfl_sync(0xFFFFFFFFu, w, 0);
       __syncwarp();
       return w != 0;
@@ -434,20 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.piece_full[pb]);
-      // ---- its queries
-      if (pieces >= 1 && !(ok = wait(&ms.q_empty, (pieces - 1) & 1))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&ms.q_full, 9 * N * 128);
-        for (int c = 0; c < 9; ++c)
-          tma_load_2d(smem + C::kOffQ + c * N * 128, &tmap_q, &ms.q_full, c * 64, static_cast<int>(row0));
-      }
-      __syncwarp();
-      ++pieces;
       // ---- its tiles: lane ↔ keys 4·lane … 4·lane + 3.  The positions of tile
       // t + 2 and the page numbers of tile t + 1 are fetched while tile t is issued
       const int32_t* sel = p.indices ? p.indices + (static_cast<int64_t>(b) * p.n + tok) * p.k : nullptr;
       const int32_t* pages = p.table + static_cast<int64_t>(b) * p.max_pages;
       const int nkeys = p.indices ? p.k : s.ctx;           // keys before the drafts
+      auto page_of = [&](int pos) {
+        return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.div_mul >> p.div_shift);
+      };
       auto position = [&](int t, int e) {                  // position of a key, −1 where it selects nothing
         const int v = t * kTile + 4 * lane + e;
         if (v >= nkeys) return v - nkeys < s.cnt && ((any >> (v - nkeys)) & 1) ? s.ctx + v - nkeys : -1;
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        page_next[e] = pos_next[e] >= 0 ? __ldg(pages + static_cast<unsigned>(pos_next[e]) / static_cast<unsigned>(p.page_size)) : 0;
+        page_next[e] = pos_next[e] >= 0 ? __ldg(pages + page_of(pos_next[e])) : 0;
       for (int t = t0; t < t1 && ok; ++t) {
         int row[4];
         uint32_t kinds = 0;
@@ -479,62 +486,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (page_next[e] < 0 || page_next[e] >= p.num_pages) {
               bad = true;
             } else {
-              row[e] = page_next[e] * p.page_size + static_cast<unsigned>(pos_next[e]) % static_cast<unsigned>(p.page_size);
+              row[e] = (page_next[e] - page_of(pos_next[e])) * p.page_size + pos_next[e];
               kinds |= static_cast<uint32_t>(v < nkeys ? 1 : 2 + v - nkeys) << (8 * e);
             }
           }
         }
         if (bad) raise_error(p.err, IDX_DEV_ERR_PAGE);
-        const bool boxes = p.box_rows && !sel && (t + 1) * kTile <= s.ctx && !__any_sync(0xFFFFFFFFu, bad);
         if (t + 1 < t1) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             pos_next[e] = valid(t + 1, e, pos_far[e]) ? pos_far[e] : -1;
-            page_next[e] = pos_next[e] >= 0 ? __ldg(pages + static_cast<unsigned>(pos_next[e]) / static_cast<unsigned>(p.page_size)) : 0;
+            page_next[e] = pos_next[e] >= 0 ? __ldg(pages + page_of(pos_next[e])) : 0;
             pos_far[e] = position(t + 2, e);
           }
         }
-        // first row of the box this lane issues: boxes of box_rows keys, chunk-major
-        const int nbox = boxes ? kTile / p.box_rows : 1;
-        const int box = lane & (nbox - 1);
-        const int box_row = __shfl_sync(0xFFFFFFFFu, row[0], boxes ? box * (p.box_rows / 4) : 0);
-        for (int u = 0; u < 5 && ok; ++u) {                // four latent pairs, then the rotary chunk
-          uint64_t* full;
-          uint32_t dst;
-          if (u < 4) {
-            const int sl = pairs % C::kPairs;
-            if (pairs >= C::kPairs) ok = wait(&ms.pair_empty[sl], (pairs / C::kPairs - 1) & 1);
-            full = &ms.pair_full[sl];
-            dst = smem_base + sl * kPair;
-            if (ok) ++pairs;
-          } else {
-            const int sl = ropes % C::kRopes;
-            if (ropes >= C::kRopes) ok = wait(&ms.rope_empty[sl], (ropes / C::kRopes - 1) & 1);
-            full = &ms.rope_full[sl];
-            dst = smem_base + C::kOffRope + sl * kChunk;
-            if (ok) ++ropes;
-          }
-          if (!ok) break;
-          if (u == 0) {
-            // what the keys are: this tile's slot was last read two tiles ago,
-            // before the product that freed the buffer just waited for
-            *reinterpret_cast<uint32_t*>(&ms.kind[tiles & 1][4 * lane]) = kinds;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.kind_full[tiles & 1]);
-          }
-          const int chunks = u < 4 ? 2 : 1;
-          if (lane == 0) mbar_arrive_expect_tx(full, chunks * kChunk);
-          __syncwarp();
-          if (boxes) {
-            const int bytes = p.box_rows * 128;
-            for (int i = lane / nbox; i < chunks; i += 32 / nbox)
-              tma_load_2d(smem + (dst - smem_base) + i * kChunk + box * bytes, &tmap_box, full, (2 * u + i) * 64, box_row);
-          } else {
-            for (int i = 0; i < chunks; ++i)
-              tma_gather4(dst + i * kChunk + lane * 512, &tmap_row, full, (2 * u + i) * 64, row[0], row[1], row[2], row[3]);
-          }
-        }
+        const int par = tiles & 1;
+        // free once the copies and the softmax have read what it said two tiles ago
+        if (tiles >= 2 && !(ok = wait(&ms.tile_read[par], ((tiles >> 1) - 1) & 1))) break;
+        *reinterpret_cast<uint32_t*>(&ms.kind[par][4 * lane]) = kinds;
+        *reinterpret_cast<int4*>(&ms.row[par][4 * lane]) = make_int4(row[0], row[1], row[2], row[3]);
+        if (lane == 0) ms.last[par] = 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.tile_full[par]);
         ++tiles;
+        if (t == t0) {                                     // its queries, once the last piece's are no longer read
+          if (pieces >= 1 && !(ok = wait(&ms.q_empty, (pieces - 1) & 1))) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&ms.q_full, 9 * N * 128);
+            for (int c = 0; c < 9; ++c)
+              tma_box(smem_base + C::kOffQ + c * N * 128, &tmap_q, smem_u32(&ms.q_full), c * 64, static_cast<int>(row0));
+          }
+          __syncwarp();
+          ++pieces;
+        }
       }
     }
     // the end of the list
@@ -545,20 +529,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ms.piece[pb].t0 = ms.piece[pb].t1 = 0;
         mbar_arrive(&ms.piece_full[pb]);
       }
+      const int par = tiles & 1;
+      if (ok && tiles >= 2) ok = wait(&ms.tile_read[par], ((tiles >> 1) - 1) & 1);
+      if (ok && lane == 0) {
+        ms.last[par] = 1;
+        mbar_arrive(&ms.tile_full[par]);
+      }
     }
     if (!p.whole && lane == 0) p.cuts[blockIdx.x] = cut;
-    // every copy has landed before the memory goes
-    if (lane == 0) {
+    if (lane == 0 && pieces) {                             // the queries have landed before the memory goes
       int dummy = 0;
-      if (pieces) mbar_wait(&ms.q_full, (pieces - 1) & 1, budget, &dummy, p.err);
-      for (int i = 0; i < C::kPairs; ++i) {
-        const int uses = (pairs - i + C::kPairs - 1) / C::kPairs;
-        if (pairs > i) mbar_wait(&ms.pair_full[i], (uses - 1) & 1, budget, &dummy, p.err);
-      }
-      for (int i = 0; i < C::kRopes; ++i) {
-        const int uses = (ropes - i + C::kRopes - 1) / C::kRopes;
-        if (ropes > i) mbar_wait(&ms.rope_full[i], (uses - 1) & 1, budget, &dummy, p.err);
-      }
+      mbar_wait(&ms.q_full, (pieces - 1) & 1, budget, &dummy, p.err);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -571,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t p_desc = desc_mn(smem_base + C::kOffP, kChunk);
     bool ok = true, issued = false;
     int pairs = 0, ropes = 0, tiles = 0, pieces = 0;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, budget, abort_flag, p.err); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_polling(bar, parity, budget, abort_flag, p.err); };
     while (true) {
       const int pb = pieces & 1;
       if (!(ok = wait(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
@@ -586,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = 0; u < 4 && ok; ++u) {
           const int sl = (first + u) % C::kPairs;
           if (!(ok = wait(&ms.pair_full[sl], ((first + u) / C::kPairs) & 1))) break;
+          fence_proxy_async_smem();                        // the copies wrote through the generic proxy
           tc_fence_after();
           if (elect_one()) {
             const uint64_t a = k_desc + static_cast<uint64_t>(sl * (kPair >> 4));
@@ -601,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const int rs = ropes % C::kRopes;
         if (!(ok = wait(&ms.rope_full[rs], (ropes / C::kRopes) & 1))) break;
+        fence_proxy_async_smem();
         tc_fence_after();
         if (elect_one()) {
           const uint64_t a = k_desc + static_cast<uint64_t>((C::kOffRope + rs * kChunk) >> 4);
@@ -644,20 +627,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&ms.drain, 0, budget, &dummy, p.err);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 2 + kCopyWarps) {
+    // ================================================================ copies
+    // A warp instruction copies 256 bytes of two rows: lanes 0-15 key 2·w + 8·j,
+    // lanes 16-31 the next; piece c of row r goes to (c mod 8) ^ (r mod 8) of its
+    // 128-byte row, the swizzle that the descriptors name
+    const int key0 = 2 * (warp - 2) + (lane >> 4);
+    const int piece = lane & 15;
+    const uint32_t to_pair = smem_base + (piece >> 3) * kChunk + key0 * 128 + (((piece & 7) ^ (key0 & 7)) << 4);
+    // rotary chunk: lanes ↔ four rows of 8 pieces
+    const int key1 = 4 * (warp - 2) + (lane >> 3);
+    const uint32_t to_rope = smem_base + C::kOffRope + key1 * 128 + (((lane & 7) ^ (key1 & 7)) << 4);
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
+    int pairs = 0, ropes = 0, tiles = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      int w = 1;
+      if (lane == 0) w = mbar_wait_polling(bar, parity, budget, abort_flag, p.err) ? 1 : 0;
+      w = __shfl_sync(0xFFFFFFFFu, w, 0);
+      __syncwarp();
+      return w != 0;
+    };
+    bool ok = true;
+    while (ok) {
+      const int par = tiles & 1;
+      if (!wait(&ms.tile_full[par], (tiles >> 1) & 1) || ms.last[par]) break;
+      int row[kTile / 8], rope_row[kTile / 16];
+#pragma unroll
+      for (int j = 0; j < kTile / 8; ++j) row[j] = ms.row[par][key0 + 8 * j];
+#pragma unroll
+      for (int j = 0; j < kTile / 16; ++j) rope_row[j] = ms.row[par][key1 + 16 * j];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.tile_read[par]);
+      for (int u = 0; u < 4; ++u) {
+        const int sl = pairs % C::kPairs;
+        if (pairs >= C::kPairs && !(ok = wait(&ms.pair_empty[sl], (pairs / C::kPairs - 1) & 1))) break;
+        const uint32_t to = to_pair + sl * kPair;
+        const uint8_t* src = from + u * 256 + piece * 16;
+#pragma unroll
+        for (int j = 0; j < kTile / 8; ++j)
+          cp_async16(to + j * 1024, src + static_cast<int64_t>(max(row[j], 0)) * (2 * kRow), row[j] >= 0 ? 16 : 0);
+        cp_async_arrive(&ms.pair_full[sl]);
+        ++pairs;
+      }
+      if (!ok) break;
+      const int sl = ropes % C::kRopes;
+      if (ropes >= C::kRopes && !(ok = wait(&ms.rope_empty[sl], (ropes / C::kRopes - 1) & 1))) break;
+      const uint32_t to = to_rope + sl * kChunk;
+      const uint8_t* src = from + 2 * kLat + (lane & 7) * 16;
+#pragma unroll
+      for (int j = 0; j < kTile / 16; ++j)
+        cp_async16(to + j * 2048, src + static_cast<int64_t>(max(rope_row[j], 0)) * (2 * kRow), rope_row[j] >= 0 ? 16 : 0);
+      cp_async_arrive(&ms.rope_full[sl]);
+      ++ropes;
+      ++tiles;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");       // they have landed before the memory goes
+  } else if (warp >= kFirstSoft) {
     // ================================================================ softmax
-    constexpr int kColShift = NC == 32 ? 0 : NC == 16 ? 1 : 2;
-    const int sw = warp - 2, quad = warp & 3, half = sw >> 2;
+    constexpr int kColShift = NC == 16 ? 1 : 2;
+    const int sw = warp - kFirstSoft, quad = warp & 3, part_id = sw >> 2;
     const int key = quad * 32 + lane;
     const int my_col = lane >> kColShift;                  // the column this lane keeps statistics of
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t s_addr = lanes + 4 * N + half * NC;
+    const uint32_t s_addr = lanes + 4 * N + part_id * NC;
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80000000u : 0u;
+    const float scale = fmaxf(fabsf(p.scale_log2), 1.1754944e-38f);   // (never 0 · −inf)
     uint8_t* p_row = smem + C::kOffP + key * 128;
     bool ok = true;
     int tiles = 0, pieces = 0, pairs = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       int w = 1;
-      if (lane == 0) w = mbar_wait(bar, parity, budget, abort_flag, p.err) ? 1 : 0;
+      if (lane == 0) w = mbar_wait_polling(bar, parity, budget, abort_flag, p.err) ? 1 : 0;
       w = __shfl_sync(0xFFFFFFFFu, w, 0);
       __syncwarp();
       return w != 0;
@@ -668,13 +708,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Piece pc = ms.piece[pb];
       if (pc.t0 == pc.t1) break;
       float m = -INFINITY;                                 // reference maximum of column my_col, log2 units
-      float l[NC], l2[NC];                                 // sums of the rounded and the unrounded weights
+      float l[NC];                                         // sums of this key's weights, before their rounding
 #pragma unroll
-      for (int c = 0; c < NC; ++c) l[c] = l2[c] = 0.f;
-      if (lane < NC) ms.m[sw][lane] = 0.f;
+      for (int c = 0; c < NC; ++c) l[c] = 0.f;
+      ms.m[sw][my_col] = 0.f;
       for (int t = pc.t0; t < pc.t1; ++t, ++tiles, pairs += 4) {
-        if (!(ok = wait(&ms.kind_full[tiles & 1], (tiles >> 1) & 1))) break;
+        if (!(ok = wait(&ms.tile_full[tiles & 1], (tiles >> 1) & 1))) break;
         const int kind = ms.kind[tiles & 1][key];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.tile_read[tiles & 1]);
         const bool all_seen = __all_sync(0xFFFFFFFFu, kind == 1);
         const bool drafts = __any_sync(0xFFFFFFFFu, kind >= 2);
         if (!(ok = wait(&ms.s_full, tiles & 1))) break;
@@ -683,9 +725,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld<NC>(s_addr, r);
         tmem_wait();
         regs_ready<NC>(r);
+        // the scores of a negative scale are compared with their signs turned
         float z[NC], v[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(r[c]) * p.scale_log2;
+        for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(r[c] ^ flip);
         if (!all_seen) {
           if (kind == 0) {
 #pragma unroll
@@ -694,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (drafts) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-              const uint64_t bits = ms.mask[pb][half * NC + c];
+              const uint64_t bits = ms.mask[pb][part_id * NC + c];
               if (kind >= 2 && !((bits >> (kind - 2)) & 1)) z[c] = -INFINITY;
             }
           }
@@ -702,29 +745,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < NC; ++c) v[c] = z[c];
         const float wm = reduce_columns<NC, true>(v, lane);
-        ms.wmax[tiles & 1][half][quad][my_col] = wm;
-        bar_half(half);
-        float top = ms.wmax[tiles & 1][half][0][my_col];
+        ms.wmax[tiles & 1][part_id][quad][my_col] = wm;
+        bar_part(part_id);
+        float top = ms.wmax[tiles & 1][part_id][0][my_col];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) top = fmaxf(top, ms.wmax[tiles & 1][half][w][my_col]);
+        for (int w = 1; w < 4; ++w) top = fmaxf(top, ms.wmax[tiles & 1][part_id][w][my_col]);
+        top = top == -INFINITY ? top : top * scale;
         const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
-        if (__any_sync(0xFFFFFFFFu, raise)) {              // the same in the half's four warps
+        if (__any_sync(0xFFFFFFFFu, raise)) {              // the same in the part's four warps
           const float a = !raise ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
           if (raise) m = top;
           ms.alpha[sw][my_col] = a;
           ms.m[sw][my_col] = m == -INFINITY ? 0.f : m;
           __syncwarp();
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float ac = ms.alpha[sw][c];
-            l[c] *= ac;
-            l2[c] *= ac;
-          }
+          for (int c = 0; c < NC; ++c) l[c] *= ms.alpha[sw][c];
           if (t > pc.t0) {                                 // (the scores' arrival implies the last product's end)
 #pragma unroll 1
             for (int blk = 0; blk < 4; ++blk) {
               uint32_t o[NC];
-              const uint32_t oa = lanes + blk * N + half * NC;
+              const uint32_t oa = lanes + blk * N + part_id * NC;
               tmem_ld<NC>(oa, o);
               tmem_wait();
               regs_ready<NC>(o);
@@ -739,22 +779,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < NC; c += 8) {
           uint32_t w[4];
+          const float4 m0 = *reinterpret_cast<const float4*>(&ms.m[sw][c]);
+          const float4 m1 = *reinterpret_cast<const float4*>(&ms.m[sw][c + 4]);
+          const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float p0 = ex2(z[c + 2 * e] - ms.m[sw][c + 2 * e]);
-            const float p1 = ex2(z[c + 2 * e + 1] - ms.m[sw][c + 2 * e + 1]);
+            const float p0 = ex2(fmaf(z[c + 2 * e], scale, -mm[2 * e]));
+            const float p1 = ex2(fmaf(z[c + 2 * e + 1], scale, -mm[2 * e + 1]));
             w[e] = bf_pack(p0, p1);
-            l2[c + 2 * e] += p0;
-            l2[c + 2 * e + 1] += p1;
-            l[c + 2 * e] += __uint_as_float(w[e] << 16);
-            l[c + 2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
+            l[c + 2 * e] += p0;
+            l[c + 2 * e + 1] += p1;
           }
-          *reinterpret_cast<uint4*>(p_row + (((half * NC + c) / 8) ^ (key & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(p_row + (((part_id * NC + c) / 8) ^ (key & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         // a draft's row that only some columns see must not reach the others as
         // 0 · NaN: where it is not finite it becomes zero (the columns that see
         // it have it in their weights already)
-        if (pc.mixed && drafts && half == 0) {
+        if (pc.mixed && drafts && part_id == 0) {
           for (int u = 0; u < 4 && ok; ++u)
             ok = wait(&ms.pair_full[(pairs + u) % C::kPairs], ((pairs + u) / C::kPairs) & 1);
           if (!ok) break;
@@ -781,27 +822,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the sums over all keys
-      const float s1 = reduce_columns<NC, false>(l, lane), s2 = reduce_columns<NC, false>(l2, lane);
-      ms.sum[0][half][quad][my_col] = s1;
-      ms.sum[1][half][quad][my_col] = s2;
-      bar_half(half);
-      float z1 = 0.f, z2 = 0.f;
+      ms.sum[part_id][quad][my_col] = reduce_columns<NC, false>(l, lane);
+      bar_part(part_id);
+      float z = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        z1 += ms.sum[0][half][w][my_col];
-        z2 += ms.sum[1][half][w][my_col];
-      }
+      for (int w = 0; w < 4; ++w) z += ms.sum[part_id][w][my_col];
       const bool whole = pc.slot < 0;
-      float* part = whole ? nullptr : p.part + (static_cast<int64_t>(blockIdx.x) * 2 + pc.slot) * (N * (kLat + 3));
-      ms.alpha[sw][my_col] = whole ? (z1 == 0.f ? 0.f : 1.f / z1) : 1.f;
+      float* part = whole ? nullptr : p.part + (static_cast<int64_t>(blockIdx.x) * 2 + pc.slot) * (N * (kLat + 2));
+      ms.alpha[sw][my_col] = whole ? (z == 0.f ? 0.f : 1.f / z) : 1.f;
       if (quad == 0 && (lane & ((1 << kColShift) - 1)) == 0) {
-        const int c = half * NC + my_col;
+        const int c = part_id * NC + my_col;
         if (!whole) {
           part[N * kLat + c] = m;
-          part[N * kLat + N + c] = z1;
-          part[N * kLat + 2 * N + c] = z2;
+          part[N * kLat + N + c] = z;
         } else if (p.lse && c < pc.rows) {
-          p.lse[pc.row0 + c] = m == -INFINITY && z2 == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * kLn2) + logf(z2);
+          p.lse[pc.row0 + c] = m == -INFINITY && z == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * kLn2) + logf(z);
         }
       }
       __syncwarp();
@@ -810,14 +845,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int blk = 0; blk < 4; ++blk) {
         uint32_t o[NC];
-        tmem_ld<NC>(lanes + blk * N + half * NC, o);
+        tmem_ld<NC>(lanes + blk * N + part_id * NC, o);
         tmem_wait();
         regs_ready<NC>(o);
         const int d = blk * 128 + key;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const float x = __uint_as_float(o[c]) * ms.alpha[sw][c];
-          const int col = half * NC + c;
+          const int col = part_id * NC + c;
           if (!whole) {
             part[col * kLat + d] = x;
           } else if (col < pc.rows) {
@@ -852,20 +887,20 @@ constexpr int kJoinGroups = 4, kJoinY = 8;
 template <int N>
 __global__ void __launch_bounds__(kJoinGroups * 128) tree_mla_join_kernel(const TreeParams p) {
   __shared__ float4 acc[kJoinGroups][128];
-  __shared__ float sums[kJoinGroups][2];
+  __shared__ float sums[kJoinGroups];
   const Cut cut = p.cuts[blockIdx.x];
   if (!cut.pieces) return;
   const int group = threadIdx.x >> 7, d = threadIdx.x & 127;
   const int team = blockIdx.x / p.team, rank = blockIdx.x % p.team;
   auto slot = [&](int i) {                     // piece 0 is this team's slot 1, the others the next teams' slot 0
-    return p.part + (static_cast<int64_t>((team + i) * p.team + rank) * 2 + (i == 0 ? 1 : 0)) * (N * (kLat + 3));
+    return p.part + (static_cast<int64_t>((team + i) * p.team + rank) * 2 + (i == 0 ? 1 : 0)) * (N * (kLat + 2));
   };
   for (int c = blockIdx.y; c < cut.rows; c += kJoinY) {
     float top = -INFINITY;
     for (int i = 0; i <= cut.pieces; ++i) top = fmaxf(top, slot(i)[N * kLat + c]);
     const float base = top == -INFINITY ? 0.f : top;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float z1 = 0.f, z2 = 0.f;
+    float z = 0.f;
 #pragma unroll 4
     for (int i = group; i <= cut.pieces; i += kJoinGroups) {
       const float* s = slot(i);
@@ -875,17 +910,13 @@ __global__ void __launch_bounds__(kJoinGroups * 128) tree_mla_join_kernel(const 
       o.y += w * x.y;
       o.z += w * x.z;
       o.w += w * x.w;
-      z1 += w * s[N * kLat + N + c];
-      z2 += w * s[N * kLat + 2 * N + c];
+      z += w * s[N * kLat + N + c];
     }
     acc[group][d] = o;
-    if (d == 0) {
-      sums[group][0] = z1;
-      sums[group][1] = z2;
-    }
+    if (d == 0) sums[group] = z;
     __syncthreads();
     if (group == 0) {
-      z1 = z2 = 0.f;
+      z = 0.f;
       o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int g = 0; g < kJoinGroups; ++g) {
@@ -894,10 +925,9 @@ __global__ void __launch_bounds__(kJoinGroups * 128) tree_mla_join_kernel(const 
         o.y += x.y;
         o.z += x.z;
         o.w += x.w;
-        z1 += sums[g][0];
-        z2 += sums[g][1];
+        z += sums[g];
       }
-      const float inv = z1 == 0.f ? 0.f : 1.f / z1;
+      const float inv = z == 0.f ? 0.f : 1.f / z;
       const int64_t at = (cut.row0 + c) * kLat + d * 4;
       if (p.out_bf16)
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
@@ -905,7 +935,7 @@ __global__ void __launch_bounds__(kJoinGroups * 128) tree_mla_join_kernel(const 
       else
         *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      if (p.lse && d == 0) p.lse[cut.row0 + c] = top == -INFINITY && z2 == 0.f ? -INFINITY : base * kLn2 + logf(z2);
+      if (p.lse && d == 0) p.lse[cut.row0 + c] = top == -INFINITY && z == 0.f ? -INFINITY : base * kLn2 + logf(z);
     }
     __syncthreads();
   }
@@ -930,17 +960,16 @@ Plan plan_for(int n, int H, int max_len, int k, int sms) {
   const int64_t tiles = ((k ? static_cast<int64_t>(k) + n : max_len) + kTile - 1) / kTile;
   pl.whole = tiles <= kMinShare || pl.teams == 1;
   const size_t ctas = static_cast<size_t>(pl.teams) * pl.team;
-  pl.ws = pl.whole ? 0 : ctas * 2 * pl.N * (kLat + 3) * sizeof(float) + ctas * sizeof(Cut);
+  pl.ws = pl.whole ? 0 : ctas * 2 * pl.N * (kLat + 2) * sizeof(float) + ctas * sizeof(Cut);
   return pl;
 }
 
 template <int N>
-int launch(const CUtensorMap& tq, const CUtensorMap& trow, const CUtensorMap& tbox, const TreeParams& p, int ctas,
-           cudaStream_t stream) {
+int launch(const CUtensorMap& tq, const TreeParams& p, int ctas, cudaStream_t stream) {
   constexpr int smem = 1024 + Cfg<N>::kOffMisc + static_cast<int>(sizeof(Misc<N>));
   static_assert(smem <= 227 * 1024, "shared memory");
   if (const int r = ensure_smem_limit(reinterpret_cast<const void*>(tree_mla_kernel<N>), smem)) return r;
-  tree_mla_kernel<N><<<static_cast<unsigned>(ctas), kThreads, smem, stream>>>(tq, trow, tbox, p);
+  tree_mla_kernel<N><<<static_cast<unsigned>(ctas), Cfg<N>::kThreads, smem, stream>>>(tq, p);
   if (const int r = check_launch()) return r;
   if (p.whole) return IDX_OK;
   tree_mla_join_kernel<N><<<dim3(static_cast<unsigned>(ctas), kJoinY), kJoinGroups * 128, 0, stream>>>(p);
@@ -983,21 +1012,20 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
   if (pl.ws > 0 && !ws) return IDX_ERR_NULL;
   if (ws_bytes < pl.ws) return IDX_ERR_SCRATCH;
   const int ctas = pl.teams * pl.team;
-  // whole runs of a page in one copy where pages are multiples of 16 rows
-  int box = page_size % 16 ? 0 : 16;
-  while (box && box < kTile && page_size % (2 * box) == 0) box *= 2;
-  CUtensorMap tq, trow, tbox;
-  const uint64_t cache_rows = static_cast<uint64_t>(num_pages) * page_size;
-  if (!make_tmap_2d_bf16_sw128(&tq, q, kRow, static_cast<uint64_t>(rows) * H, static_cast<uint32_t>(pl.N)) ||
-      !make_tmap_2d_bf16_sw128(&trow, cache, kRow, cache_rows, 1) ||
-      !make_tmap_2d_bf16_sw128(&tbox, cache, kRow, cache_rows, static_cast<uint32_t>(box ? box : 1)))
+  CUtensorMap tq;
+  if (!make_tmap_2d_bf16_sw128(&tq, q, kRow, static_cast<uint64_t>(rows) * H, static_cast<uint32_t>(pl.N)))
     return IDX_ERR_UNSUPPORTED;
   TreeParams p;
   p.table = page_table;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.page_size = page_size;
-  p.box_rows = box;
+  p.cache = cache;
+  // s = ⌈log2 d⌉, m = ⌊2^(31+s)/d⌋ + 1: x·m >> (31+s) is x / d for every x < 2^31
+  int sh = 0;
+  while ((int64_t{1} << sh) < page_size) ++sh;
+  p.div_mul = static_cast<uint32_t>((uint64_t{1} << (31 + sh)) / static_cast<uint64_t>(page_size) + 1);
+  p.div_shift = 31 + sh;
   p.lengths = lengths;
   p.counts = counts;
   p.B = B;
@@ -1017,12 +1045,12 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
   p.whole = pl.whole;
   p.part = static_cast<float*>(ws);
   p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(ws) +
-                                  static_cast<size_t>(ctas) * 2 * pl.N * (kLat + 3) * sizeof(float));
+                                  static_cast<size_t>(ctas) * 2 * pl.N * (kLat + 2) * sizeof(float));
   p.budget_ns = debug_state().budget_ns;
   p.err = device_error_word();
   if (!p.err) return check_launch();
   auto* s = reinterpret_cast<cudaStream_t>(stream);
-  return pl.N == 16   ? launch<16>(tq, trow, tbox, p, ctas, s)
-         : pl.N == 32 ? launch<32>(tq, trow, tbox, p, ctas, s)
-                      : launch<64>(tq, trow, tbox, p, ctas, s);
+  return pl.N == 16   ? launch<16>(tq, p, ctas, s)
+         : pl.N == 32 ? launch<32>(tq, p, ctas, s)
+                      : launch<64>(tq, p, ctas, s);
 }
