@@ -1,0 +1,506 @@
+// What the two kernels of idx_tree_mla share: the call's parameters, how its work
+// is dealt to the CTAs, the planner warp that walks a CTA's share, the join of
+// items that shares cut, and inline PTX.
+//
+// Work: an item is a row block of a sequence (of a token, where each token has
+// its own selection) with all keys that it sees, in tiles of KT keys.  The tiles
+// of all items are numbered through and dealt in equal contiguous shares to teams
+// of CTAs, one persistent CTA per SM; the CTAs of a team walk the same tiles with
+// different rows or output columns, so a tile comes from HBM once and from L2
+// after that.  An item that a share's end cuts leaves partial (O, maximum, sum)
+// in the workspace, and tree_mla_join adds them in a fixed order.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cmath>
+#include <cstdint>
+
+#include "api_internal.h"
+#include "ptx.cuh"
+
+namespace idx {
+namespace tree {
+
+constexpr int kLat = 512, kRow = 576;
+constexpr int kMinShare = 256;                // keys per share below which work is not split further
+constexpr float kRaise = 8.f;                 // log2 margin of the reference maximum
+constexpr float kNone = -3.0e38f;             // stands for a reference maximum of −inf: any score passes it
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct Piece {                                // what the CTA does next: tiles [t0, t1) of an item
+  int t0, t1;
+  int rows;                                   // valid rows
+  int slot;                                   // −1: the whole item; else partial slot 0 or 1
+  int mixed;                                  // the rows belong to several tokens
+  int nkeys;                                  // keys before the drafts
+  int64_t row0;                               // global row of the first
+};
+
+struct Cut {                                  // an item that begins in a share and ends in another
+  int64_t row0;
+  int rows, pieces;                           // pieces after the first; 0: nothing to join
+};
+
+struct TreeParams {
+  const uint16_t *q, *cache;
+  const int32_t* table;
+  int max_pages, num_pages, page_size;
+  uint32_t div_mul;                           // x / page_size = x · div_mul >> div_shift for x < 2^31
+  int div_shift;
+  const int32_t *lengths, *counts;
+  int B, n, H, max_len;
+  const uint64_t* mask;
+  const int32_t* indices;
+  int k;
+  float scale_log2;
+  void* out;
+  int out_bf16;
+  float* lse;
+  int M, halves;                              // rows per CTA; CTAs that share the output columns of a row
+  int team, blocks;                           // CTAs per team, row blocks (of a team's rows) per token set
+  int teams, whole;                           // whole: items are not cut
+  float* part;                                // [CTA][2] partial slots: M · (512 / halves) outputs, M maxima, M sums
+  Cut* cuts;                                  // [CTA]
+  unsigned long long budget_ns;
+  unsigned int* err;
+};
+
+int launch_tree_mla_wide(const CUtensorMap& tmap_q, const TreeParams& p, int ctas, cudaStream_t stream);
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// mbar_wait that polls 256 times before it looks at the clock: a read of the
+// global timer takes about 1 000 cycles, which every wait that does not succeed
+// at once would add to its hand-off
+__device__ __forceinline__ bool mbar_wait_polling(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
+                                                  volatile int* abort_flag, unsigned int* err) {
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, budget_ns, abort_flag, err);
+}
+// 16 bytes into shared memory, zeros where bytes = 0; cp_async_arrive makes the
+// barrier count this thread once its copies so far have landed
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// the same with A read from TMEM (row m in lane m, two bf16 per 32-bit column)
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// kind::f16, A = B = bf16, D = f32, M = 128; a_mn, b_mn: operand MN-major
+__host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? (1u << 15) : 0u) | (b_mn ? (1u << 16) : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+constexpr uint32_t kNegateA = 1u << 13;       // the product with A's signs turned
+// MN-major operand, 128-byte swizzle: 64 elements along MN per 128-byte row, 8-row
+// atoms along K; `mn_stride` bytes to the next 64 elements along MN
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t mn_stride) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | static_cast<uint64_t>((mn_stride >> 4) & 0x3FFF) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two weights (≥ 0) rounded to bf16, ties away from zero: on the integer pipe,
+// since the conversion instruction shares its pipe with ex2 and 8 192 of each per
+// tile are what the softmax would wait for.  A NaN weight may be lost here; its
+// row's sum keeps it.
+__device__ __forceinline__ uint32_t bf_pack_weights(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo) + 0x8000u, __float_as_uint(hi) + 0x8000u, 0x7632);
+}
+// `count` threads meet; whether any of them says v
+__device__ __forceinline__ void bar_named(int id, int count) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_named_any(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+// every lane polls, or lane 0 for its warp; false once the CTA has given up
+struct Waits {
+  uint64_t budget;
+  volatile int* abort_flag;
+  unsigned int* err;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    return mbar_wait_polling(bar, parity, budget, abort_flag, err);
+  }
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+    int w = 1;
+    if ((threadIdx.x & 31) == 0) w = mbar_wait_polling(bar, parity, budget, abort_flag, err) ? 1 : 0;
+    w = __shfl_sync(0xFFFFFFFFu, w, 0);
+    __syncwarp();
+    return w != 0;
+  }
+  // during teardown: whatever happened before, wait for what is in flight
+  __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
+    int dummy = 0;
+    mbar_wait(bar, parity, budget, &dummy, err);
+  }
+};
+
+// NC consecutive 32-bit columns of this warp's 32 lanes
+template <int NC>
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t* r);
+template <>
+__device__ __forceinline__ void tmem_ld<8>(uint32_t a, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a));
+}
+template <>
+__device__ __forceinline__ void tmem_ld<16>(uint32_t a, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+template <int NC>
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t* r);
+template <>
+__device__ __forceinline__ void tmem_st<8>(uint32_t a, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_st<16>(uint32_t a, const uint32_t* r) {
+  tmem_st<8>(a, r);
+  tmem_st<8>(a + 8, r + 8);
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// ties loaded registers to a point after tmem_wait()
+template <int NC>
+__device__ __forceinline__ void regs_ready(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < NC; i += 8)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+// ------------------------------------------------------------------ work
+struct Seq {
+  int len, cnt, ctx, items, tiles;            // items: row blocks to serve; tiles per item
+};
+template <int KT>
+__device__ __forceinline__ Seq seq_info(const TreeParams& p, int b, bool report) {
+  Seq s;
+  s.cnt = p.counts ? __ldg(p.counts + b) : p.n;
+  s.len = __ldg(p.lengths + b);
+  if (s.cnt < 0 || s.cnt > p.n || s.len < s.cnt || s.len > p.max_len) {
+    if (report) raise_error(p.err, IDX_DEV_ERR_LENGTH);
+    s.cnt = s.len = 0;
+  }
+  s.ctx = s.len - s.cnt;
+  s.items = p.indices ? s.cnt * p.blocks : s.cnt > 0 ? p.blocks : 0;
+  s.tiles = (static_cast<int>(p.indices ? p.k + s.cnt : s.len) + KT - 1) / KT;
+  return s;
+}
+
+// drafts that a token's rows see
+__device__ __forceinline__ uint64_t draft_mask(const TreeParams& p, int b, int i, int cnt) {
+  const uint64_t all = cnt >= 64 ? ~0ull : (1ull << cnt) - 1;
+  const uint64_t m = p.mask ? __ldg(reinterpret_cast<const unsigned long long*>(p.mask) + static_cast<int64_t>(b) * p.n + i)
+                            : (2ull << i) - 1;
+  return m & all;
+}
+
+// Shared state of the planner and the warps that follow it; M rows, KT keys a tile.
+template <int M, int KT, int kWarps>
+struct PlanState {
+  uint64_t mask[2][M];                        // per piece parity: drafts each row sees
+  alignas(16) uint8_t kind[2][KT];            // per tile parity and key: 0 unseen, 1 context, 2 + j draft j
+  alignas(16) int row[2][KT];                 // per tile parity: cache rows of the keys, −1: none
+  int last[2];                                // per tile parity: no tile, the list has ended
+  Piece piece[2];
+  long long scan[kWarps];
+  long long start_off;
+  int start_b;
+  int abort_flag;
+  uint32_t tmem;
+  uint64_t tile_full[2], tile_read[2], piece_full[2], piece_empty[2], q_full, q_empty;
+
+  __device__ void init(int B, int tile_readers, int piece_readers) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tile_full[i], 1);
+      mbar_init(&tile_read[i], tile_readers);
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], piece_readers);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    abort_flag = 0;
+    start_b = B;
+    start_off = 0;
+  }
+};
+
+struct Share {
+  long long size, begin, end;                 // in tiles (in items where they are not cut)
+};
+// Where this team's share lies: every thread of the CTA adds up a run of
+// sequences, then the one whose run holds the share's begin looks for it.  Two
+// CTA barriers; what was written before the first is visible after it.
+template <int KT, int kThreads, class State>
+__device__ __forceinline__ Share find_share(const TreeParams& p, State& ms, int team) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Seq s = seq_info<KT>(p, b, blockIdx.x == 0);
+    mine += static_cast<long long>(s.items) * (p.whole ? 1 : s.tiles);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) ms.scan[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0, before = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += ms.scan[w];
+    total += ms.scan[w];
+  }
+  Share sh;
+  sh.size = max(static_cast<long long>(p.whole ? 1 : kMinShare / KT), (total + p.teams - 1) / p.teams);
+  sh.begin = min(total, sh.size * team);
+  sh.end = min(total, sh.begin + sh.size);
+  if (sh.begin < sh.end && before + incl - mine <= sh.begin && sh.begin < before + incl) {
+    long long at = before + incl - mine;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const Seq s = seq_info<KT>(p, b, false);
+      const long long w = static_cast<long long>(s.items) * (p.whole ? 1 : s.tiles);
+      if (sh.begin < at + w) {
+        ms.start_b = b;
+        ms.start_off = sh.begin - at;
+        break;
+      }
+      at += w;
+    }
+  }
+  __syncthreads();
+  return sh;
+}
+
+// The planner warp: walks the share, publishes each piece (tile range, what its
+// rows see of the drafts) and each tile (cache rows of its keys), and has the
+// piece's queries loaded: load_q(row0) issues them on ms.q_full.
+template <int M, int KT, class State, class LoadQ>
+__device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share& sh, int rank, const Waits& waits,
+                                     LoadQ load_q) {
+  constexpr int E = KT / 32;                  // keys per lane
+  const int lane = threadIdx.x & 31;
+  bool ok = true;
+  int tiles = 0, pieces = 0;                  // running counts
+  long long cur = sh.begin;
+  int b = ms.start_b;
+  long long off = ms.start_off;
+  Cut cut{0, 0, 0};
+  Seq s{};
+  if (b < p.B) s = seq_info<KT>(p, b, false);
+  while (ok && cur < sh.end) {
+    const int weight = p.whole ? 1 : s.tiles;
+    if (off >= static_cast<long long>(s.items) * weight) {
+      if (++b >= p.B) break;
+      s = seq_info<KT>(p, b, false);
+      off = 0;
+      continue;
+    }
+    const int item = static_cast<int>(off / weight);
+    const int t0 = p.whole ? 0 : static_cast<int>(off - static_cast<long long>(item) * weight);
+    const int t1 = p.whole ? s.tiles : static_cast<int>(min(static_cast<long long>(s.tiles), t0 + (sh.end - cur)));
+    const int step = p.whole ? 1 : t1 - t0;
+    off += step;
+    cur += step;
+    // this CTA's rows: M flattened (token, head) rows of the sequence, or M heads
+    // of one token where each token has its selection
+    const int tok = p.indices ? item / p.blocks : 0;
+    const int blk = p.indices ? item % p.blocks : item;
+    const int64_t lo = (static_cast<int64_t>(blk) * (p.team / p.halves) + rank / p.halves) * M;
+    const int64_t have = p.indices ? p.H : static_cast<int64_t>(s.cnt) * p.H;
+    const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(M), have - lo)));
+    const int64_t row0 = (static_cast<int64_t>(b) * p.n + tok) * p.H + lo;
+    const int slot = t0 == 0 && t1 == s.tiles ? -1 : t0 == 0 ? 1 : 0;
+    if (slot == 1) {
+      cut.row0 = row0;
+      cut.rows = rows;
+      cut.pieces = static_cast<int>((s.tiles - t1 + sh.size - 1) / sh.size);
+    }
+    if (rows == 0) continue;                  // the team has more rows than this sequence
+    const int nkeys = p.indices ? p.k : s.ctx;
+    const int pb = pieces & 1;
+    if (pieces >= 2 && !(ok = waits.warp(&ms.piece_empty[pb], ((pieces >> 1) - 1) & 1))) break;
+    uint64_t any = 0;
+    for (int c = lane; c < M; c += 32) {
+      const uint64_t m = c < rows ? draft_mask(p, b, p.indices ? tok : static_cast<int>((lo + c) / p.H), s.cnt) : 0;
+      ms.mask[pb][c] = m;
+      any |= m;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) any |= __shfl_xor_sync(0xFFFFFFFFu, any, o);
+    if (lane == 0) {
+      Piece& pc = ms.piece[pb];
+      pc.t0 = t0;
+      pc.t1 = t1;
+      pc.rows = rows;
+      pc.slot = slot;
+      pc.mixed = !p.indices && lo / p.H != (lo + rows - 1) / p.H;
+      pc.nkeys = nkeys;
+      pc.row0 = row0;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ms.piece_full[pb]);
+    // ---- its tiles: lane ↔ keys E·lane …  The positions of tile t + 2 and the
+    // page numbers of tile t + 1 are fetched while tile t is published
+    const int32_t* sel = p.indices ? p.indices + (static_cast<int64_t>(b) * p.n + tok) * p.k : nullptr;
+    const int32_t* pages = p.table + static_cast<int64_t>(b) * p.max_pages;
+    auto page_of = [&](int pos) {
+      return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.div_mul >> p.div_shift);
+    };
+    auto position = [&](int t, int e) {       // position of a key, −1 where it selects nothing
+      const int v = t * KT + E * lane + e;
+      if (v >= nkeys) return v - nkeys < s.cnt && ((any >> (v - nkeys)) & 1) ? s.ctx + v - nkeys : -1;
+      if (!sel) return v;
+      return t < t1 ? __ldg(sel + v) : -1;
+    };
+    auto valid = [&](int t, int e, int pos) {  // a selection names context positions only
+      return pos >= 0 && (t * KT + E * lane + e >= nkeys || pos < s.ctx);
+    };
+    int pos_next[E], page_next[E], pos_far[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      pos_next[e] = position(t0, e);
+      if (!valid(t0, e, pos_next[e])) pos_next[e] = -1;
+      pos_far[e] = position(t0 + 1, e);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) page_next[e] = pos_next[e] >= 0 ? __ldg(pages + page_of(pos_next[e])) : 0;
+    for (int t = t0; t < t1; ++t) {
+      int row[E];
+      uint32_t kinds = 0;
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int v = t * KT + E * lane + e;
+        row[e] = -1;
+        if (pos_next[e] >= 0) {
+          if (page_next[e] < 0 || page_next[e] >= p.num_pages) {
+            bad = true;
+          } else {
+            row[e] = (page_next[e] - page_of(pos_next[e])) * p.page_size + pos_next[e];
+            kinds |= static_cast<uint32_t>(v < nkeys ? 1 : 2 + v - nkeys) << (8 * e);
+          }
+        }
+      }
+      if (bad) raise_error(p.err, IDX_DEV_ERR_PAGE);
+      if (t + 1 < t1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          pos_next[e] = valid(t + 1, e, pos_far[e]) ? pos_far[e] : -1;
+          page_next[e] = pos_next[e] >= 0 ? __ldg(pages + page_of(pos_next[e])) : 0;
+          pos_far[e] = position(t + 2, e);
+        }
+      }
+      const int par = tiles & 1;
+      // free once the copies and the softmax have read what it said two tiles ago
+      if (tiles >= 2 && !(ok = waits.warp(&ms.tile_read[par], ((tiles >> 1) - 1) & 1))) break;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        ms.kind[par][E * lane + e] = static_cast<uint8_t>(kinds >> (8 * e));
+        ms.row[par][E * lane + e] = row[e];
+      }
+      if (lane == 0) ms.last[par] = 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.tile_full[par]);
+      ++tiles;
+      if (t == t0) {                          // its queries, once the last piece's are no longer read
+        if (pieces >= 1 && !(ok = waits.warp(&ms.q_empty, (pieces - 1) & 1))) break;
+        if (elect_one()) load_q(static_cast<int>(row0));
+        __syncwarp();
+        ++pieces;
+      }
+    }
+  }
+  // the end of the list
+  if (ok) {
+    const int pb = pieces & 1;
+    if (pieces >= 2) ok = waits.warp(&ms.piece_empty[pb], ((pieces >> 1) - 1) & 1);
+    if (ok && lane == 0) {
+      ms.piece[pb].t0 = ms.piece[pb].t1 = 0;
+      mbar_arrive(&ms.piece_full[pb]);
+    }
+    const int par = tiles & 1;
+    if (ok && tiles >= 2) ok = waits.warp(&ms.tile_read[par], ((tiles >> 1) - 1) & 1);
+    if (ok && lane == 0) {
+      ms.last[par] = 1;
+      mbar_arrive(&ms.tile_full[par]);
+    }
+  }
+  if (!p.whole && lane == 0) p.cuts[blockIdx.x] = cut;
+  if (lane == 0 && pieces) waits.drain(&ms.q_full, (pieces - 1) & 1);   // landed before the memory goes
+  __syncwarp();
+}
+
+__device__ __forceinline__ float lse_of(float m, float z) {    // m in log2 units
+  return m == -INFINITY && z == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * kLn2) + logf(z);
+}
+
+// partial slot of a CTA: M rows of D outputs, M maxima, M sums
+__device__ __forceinline__ float* part_slot(const TreeParams& p, int64_t cta, int slot) {
+  return p.part + (cta * 2 + slot) * (static_cast<int64_t>(p.M) * (kLat / p.halves + 2));
+}
+
+}  // namespace tree
+}  // namespace idx

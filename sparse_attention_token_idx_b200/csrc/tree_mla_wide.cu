@@ -1,0 +1,469 @@
+// Latent attention of drafted token trees over the paged cache (idx_tree_mla),
+// for more than 64 rows per set of keys (tokens · heads, or heads where each
+// token has its own selection): groups of 128 rows.
+//
+// A row is an accumulator lane: S = q · Kᵀ (M = 128 rows, N = 64 keys, K = 576)
+// and O = P · V (N = 256 output features, K = 64 keys).  TMEM holds 512 columns,
+// and a full O of 512 would leave none for S, so two CTAs share a row group: both
+// compute all its scores (36 MMAs per tile: 24 with the queries in TMEM at 32
+// cycles, 12 with them in shared memory at 48) and each accumulates its half of
+// the output features (4 MMAs at 128), 1 860 cycles per 64 keys where one CTA
+// with a whole S and O would need 2 180 of the tensor cores.
+//
+// The tile's nine 64-feature chunks live in two rings: the four that are also
+// this CTA's V (three buffers: free after the product) and the five others (a ring
+// of seven: free after the scores).  So the copies of the next tile wait neither
+// for this tile's softmax nor for its product, and the MMA warp issues the scores of
+// tile t + 1 before the product of tile t: the softmax of t runs under them.
+//
+// One CTA, 18 warps:
+//   warp 0       the planner (tree_mla.cuh);
+//   warp 1       issues the MMAs;
+//   warps 2-9    copy the rows by cp.async, 16 bytes a lane (a key that no row sees
+//                arrives as zeros);
+//   warps 10-17  softmax: thread ↔ (row, half of the keys), the row's reference
+//                maximum in a register, raised only where a score passes it by 2^8
+//                (then the two threads of a row agree through shared memory and O
+//                in TMEM is rescaled); P = 2^(s − m) in bf16 in shared memory;
+//                between pieces they put the next queries' first six chunks into
+//                TMEM while the last product runs.
+// Rounding, bounded waits and the way out as in tree_mla.cu.
+#include "tree_mla.cuh"
+
+namespace idx {
+namespace {
+
+using namespace tree;
+
+constexpr int kRows = 128;                    // rows per CTA
+constexpr int kKeys = 64;                     // keys per tile
+constexpr int kHalf = 256;                    // output features per CTA
+constexpr int kCopyWarps = 8, kSoftWarps = 8;
+constexpr int kFirstSoft = 2 + kCopyWarps;
+constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
+constexpr int kChunk = kKeys * 128;           // 64 keys × 64 features
+constexpr int kV = 4 * kChunk;                // a V buffer
+constexpr int kVs = 3, kXs = 7;               // buffers of V, and of the other chunks
+constexpr int kQTmem = 6;                     // query chunks in TMEM; the other three in shared memory
+constexpr int kQChunk = kRows * 128;
+
+constexpr int kOffX = kVs * kV;
+constexpr int kOffQ = kOffX + kXs * kChunk;
+constexpr int kOffP = kOffQ + 3 * kQChunk;
+constexpr int kOffMisc = kOffP + kRows * 128;
+constexpr uint32_t kColS = kQTmem * 32, kColO = 256;
+static_assert(kColS + kKeys <= kColO, "TMEM columns");
+
+struct WideState : PlanState<kRows, kKeys, kThreads / 32> {
+  float top[2][kRows], sum[2][kRows];         // per half of the keys
+  uint64_t v_full[kVs], v_empty[kVs], x_full[kXs], x_empty[kXs];
+  uint64_t q_ready, s_full, s_free, p_full, p_free, o_full, o_free, drain_bar;
+};
+constexpr int kSmem = 1024 + kOffMisc + static_cast<int>(sizeof(WideState));
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+// The chunks in the order the scores take them: the four latent chunks of the
+// other half, the rotary chunk, the four of this half.
+__device__ __forceinline__ int feature_chunk(int pos, int half) {
+  return pos < 4 ? 4 * (1 - half) + pos : pos == 4 ? 8 : 4 * half + pos - 5;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_mla_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const TreeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  WideState& ms = *reinterpret_cast<WideState*>(smem + kOffMisc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = blockIdx.x / p.team, rank = blockIdx.x % p.team;
+  const int half = rank & 1;
+  const Waits waits{p.budget_ns, &ms.abort_flag, p.err};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kVs; ++i) {
+      mbar_init(&ms.v_full[i], kCopyWarps * 32);
+      mbar_init(&ms.v_empty[i], 1);
+    }
+    for (int i = 0; i < kXs; ++i) {
+      mbar_init(&ms.x_full[i], kCopyWarps * 32);
+      mbar_init(&ms.x_empty[i], 1);
+    }
+    mbar_init(&ms.q_ready, kSoftWarps);
+    mbar_init(&ms.s_full, 1);
+    mbar_init(&ms.s_free, kSoftWarps);
+    mbar_init(&ms.p_full, kSoftWarps);
+    mbar_init(&ms.p_free, 1);
+    mbar_init(&ms.o_full, 1);
+    mbar_init(&ms.o_free, kSoftWarps);
+    mbar_init(&ms.drain_bar, 1);
+    ms.init(p.B, kCopyWarps + kSoftWarps, kSoftWarps + 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tmap_q);
+  }
+  if (warp == 1) tmem_alloc(&ms.tmem, 512);
+  const Share share = find_share<kKeys, kThreads>(p, ms, team);
+  const uint32_t tmem = ms.tmem;
+  const uint32_t smem_base = smem_u32(smem);
+
+  if (warp == 0) {
+    plan<kRows, kKeys>(p, ms, share, rank, waits, [&](int row0) {
+      mbar_arrive_expect_tx(&ms.q_full, 3 * kQChunk);
+      for (int c = 0; c < 3; ++c)
+        tma_box(smem_base + kOffQ + c * kQChunk, &tmap_q, smem_u32(&ms.q_full), feature_chunk(kQTmem + c, half) * 64,
+                row0);
+    });
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer
+    const uint32_t id_s = idesc_bf16(kKeys, false, false) | (p.scale_log2 < 0.f ? kNegateA : 0u);
+    constexpr uint32_t id_o = idesc_bf16(kHalf, false, true);
+    const uint32_t d_s = tmem + kColS, d_o = tmem + kColO;
+    const uint64_t k_desc = smem_desc_k128_sw128(smem_base);
+    const uint64_t q_desc = smem_desc_k128_sw128(smem_base + kOffQ);
+    const uint64_t p_desc = smem_desc_k128_sw128(smem_base + kOffP);
+    const uint64_t v_desc = desc_mn(smem_base, kChunk);
+    bool ok = true, issued = false;
+    int xs = 0, tiles = 0, pieces = 0;         // running counts (tiles: scores issued)
+    while (true) {
+      const int pb = pieces & 1;
+      if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
+      const int n = ms.piece[pb].t1 - ms.piece[pb].t0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
+      if (n == 0) break;
+      if (!(ok = waits(&ms.q_full, pieces & 1)) || !(ok = waits(&ms.q_ready, pieces & 1))) break;
+      for (int c = 0; c <= n && ok; ++c) {
+        if (c < n) {
+          // S = q · Kᵀ of tile c, once the softmax has read the last S
+          if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
+          for (int u = 0; u < 5 && ok; ++u) ok = waits(&ms.x_full[(xs + u) % kXs], ((xs + u) / kXs) & 1);
+          if (!ok) break;
+          fence_proxy_async_smem();            // the copies wrote through the generic proxy
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int u = 0; u < 5; ++u) {
+              const int sl = (xs + u) % kXs;
+              const uint64_t b = k_desc + static_cast<uint64_t>((kOffX + sl * kChunk) >> 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + u * 32 + i * 8, b + i * 2, id_s, (u > 0 || i > 0) ? 1u : 0u);
+              mma_commit(&ms.x_empty[sl]);
+            }
+          }
+          issued = true;
+          __syncwarp();
+          xs += 5;
+          const int sl = tiles % kVs;
+          if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t b = k_desc + static_cast<uint64_t>(sl * (kV >> 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + 5 * 32 + i * 8, b + i * 2, id_s, 1u);
+#pragma unroll
+            for (int i = 0; i < 12; ++i)
+              mma_f16(d_s, q_desc + static_cast<uint64_t>((i >> 2) * (kQChunk >> 4) + (i & 3) * 2),
+                      b + static_cast<uint64_t>(((i >> 2) + 1) * (kChunk >> 4) + (i & 3) * 2), id_s, 1u);
+            mma_commit(&ms.s_full);
+            if (c == n - 1) mma_commit(&ms.q_empty);
+          }
+          __syncwarp();
+          ++tiles;
+        }
+        if (c >= 1) {
+          // O += P · V of tile c − 1
+          const int t = tiles - (c < n ? 2 : 1);
+          if (!(ok = waits(&ms.p_full, t & 1))) break;
+          if (c == 1 && pieces > 0 && !(ok = waits(&ms.o_free, (pieces - 1) & 1))) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          if (elect_one()) {
+            const int sl = t % kVs;
+            const uint64_t b = v_desc + static_cast<uint64_t>(sl * (kV >> 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)         // 16 keys per instruction: two 8-row atoms
+              mma_f16(d_o, p_desc + i * 2, b + i * (2048 >> 4), id_o, (c > 1 || i > 0) ? 1u : 0u);
+            mma_commit(&ms.p_free);
+            mma_commit(&ms.v_empty[sl]);
+            if (c == n) mma_commit(&ms.o_full);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      ++pieces;
+    }
+    if (issued) {
+      if (elect_one()) mma_commit(&ms.drain_bar);
+      __syncwarp();
+      waits.drain(&ms.drain_bar, 0);
+    }
+    __syncwarp();
+  } else if (warp < kFirstSoft) {
+    // ================================================================ copies
+    // V: a warp instruction copies 512 bytes of key w + 8·j.  The other chunks:
+    // 128 bytes of the four keys 4·w + 32·j ….  Piece c of row r goes to
+    // (c mod 8) ^ (r mod 8) of its 128-byte row, as the descriptors say.
+    const int w = warp - 2;
+    const uint32_t to_v = smem_base + (lane >> 3) * kChunk + w * 128 + (((lane & 7) ^ (w & 7)) << 4);
+    const int key1 = 4 * w + (lane >> 3);
+    const uint32_t to_x = smem_base + kOffX + key1 * 128 + (((lane & 7) ^ (key1 & 7)) << 4);
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
+    int xs = 0, tiles = 0;
+    bool ok = true;
+    while (ok) {
+      const int par = tiles & 1;
+      if (!waits.warp(&ms.tile_full[par], (tiles >> 1) & 1) || ms.last[par]) break;
+      int row[8], xrow[2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) row[j] = ms.row[par][w + 8 * j];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) xrow[j] = ms.row[par][key1 + 32 * j];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.tile_read[par]);
+      for (int u = 0; u < 5; ++u) {
+        const int sl = xs % kXs;
+        if (xs >= kXs && !(ok = waits.warp(&ms.x_empty[sl], (xs / kXs - 1) & 1))) break;
+        const uint8_t* src = from + feature_chunk(u, half) * 128 + (lane & 7) * 16;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          cp_async16(to_x + sl * kChunk + j * 4096, src + static_cast<int64_t>(max(xrow[j], 0)) * (2 * kRow),
+                     xrow[j] >= 0 ? 16 : 0);
+        cp_async_arrive(&ms.x_full[sl]);
+        ++xs;
+      }
+      if (!ok) break;
+      const int sl = tiles % kVs;
+      if (tiles >= kVs && !(ok = waits.warp(&ms.v_empty[sl], (tiles / kVs - 1) & 1))) break;
+      const uint8_t* src = from + half * 512 + lane * 16;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        cp_async16(to_v + sl * kV + j * 1024, src + static_cast<int64_t>(max(row[j], 0)) * (2 * kRow), row[j] >= 0 ? 16 : 0);
+      cp_async_arrive(&ms.v_full[sl]);
+      ++tiles;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");       // they have landed before the memory goes
+  } else {
+    // ================================================================ softmax
+    const int sw = warp - kFirstSoft, quad = warp & 3, part = sw >> 2;
+    const int r_id = quad * 32 + lane;                     // row within the group (TMEM lane)
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const float scale = fmaxf(fabsf(p.scale_log2), 1.1754944e-38f);   // (never 0 · −inf)
+    uint8_t* p_row = smem + kOffP + r_id * 128;
+    bool ok = true;
+    int tiles = 0, pieces = 0;
+    // three of the six query chunks that live in TMEM, into this warp's lanes
+    auto load_q = [&](const Piece& pc) {
+#pragma unroll 1
+      for (int i = 0; i < 3; ++i) {
+        const int pos = part * 3 + i;
+        uint32_t r[32];
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (pc.row0 + r_id) * kRow + feature_chunk(pos, half) * 64);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 x = r_id < pc.rows ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+          r[4 * j] = x.x;
+          r[4 * j + 1] = x.y;
+          r[4 * j + 2] = x.z;
+          r[4 * j + 3] = x.w;
+        }
+        tmem_st<16>(lanes + pos * 32, r);
+        tmem_st<16>(lanes + pos * 32 + 16, r + 16);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.q_ready);
+    };
+    ok = waits.warp(&ms.piece_full[0], 0);
+    if (ok && ms.piece[0].t0 != ms.piece[0].t1) load_q(ms.piece[0]);
+    while (ok) {
+      const int pb = pieces & 1;
+      const Piece pc = ms.piece[pb];
+      if (pc.t0 == pc.t1) break;
+      const uint64_t drafts = ms.mask[pb][r_id];
+      float m = -INFINITY, l = 0.f;                        // reference maximum (log2 units), sum of this half's weights
+      for (int t = pc.t0; t < pc.t1; ++t, ++tiles) {
+        // what this row sees of the tile's keys: the context, and its drafts (draft
+        // j is key nkeys + j)
+        if (!(ok = waits.warp(&ms.tile_full[tiles & 1], (tiles >> 1) & 1))) break;
+        const int k0 = ms.kind[tiles & 1][part * 32 + lane];
+        const uint32_t ctx = __ballot_sync(0xFFFFFFFFu, k0 == 1), dr = __ballot_sync(0xFFFFFFFFu, k0 >= 2);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.tile_read[tiles & 1]);
+        uint32_t sees = ctx;
+        if (dr) {
+          const int sh = pc.nkeys - (t * kKeys + part * 32);   // key of draft 0 in these 32
+          const uint64_t at = sh >= 0 ? (sh < 64 ? drafts << sh : 0) : (sh > -64 ? drafts >> -sh : 0);
+          sees |= static_cast<uint32_t>(at) & dr;
+        }
+        if (!(ok = waits.warp(&ms.s_full, tiles & 1))) break;
+        tc_fence_after();
+        uint32_t r[32];
+        tmem_ld<16>(lanes + kColS + part * 32, r);
+        tmem_ld<16>(lanes + kColS + part * 32 + 16, r + 16);
+        tmem_wait();
+        regs_ready<32>(r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.s_free);
+        float z[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) z[c] = __uint_as_float(r[c]);
+        if (__any_sync(0xFFFFFFFFu, sees != 0xFFFFFFFFu)) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!((sees >> c) & 1)) z[c] = -INFINITY;
+        }
+        float far = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) far = fmaxf(far, z[c]);
+        const float mu = m == -INFINITY ? kNone : m;
+        const bool raised = bar_named_any(1 + quad, 64, t == pc.t0 || fmaf(far, scale, -mu) > kRaise);
+        float a = 1.f;
+        if (raised) {                                      // the same in both warps of these rows
+          ms.top[part][r_id] = far;
+          bar_named(1 + quad, 64);
+          float top = fmaxf(far, ms.top[1 - part][r_id]);
+          top = top == -INFINITY ? top : top * scale;
+          const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
+          if (raise) {
+            a = m == -INFINITY ? 0.f : ex2(m - top);
+            m = top;
+          }
+          l *= a;
+          bar_named(1 + quad, 64);                         // (top may be written again)
+        }
+        const float base = m == -INFINITY ? kNone : m;
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float p0 = ex2(fmaf(z[2 * c], scale, -base)), p1 = ex2(fmaf(z[2 * c + 1], scale, -base));
+          w[c] = bf_pack_weights(p0, p1);
+          l += p0 + p1;
+        }
+        // P and O are free once the last product has ended
+        if (tiles >= 1 && !(ok = waits.warp(&ms.p_free, (tiles - 1) & 1))) break;
+        tc_fence_after();
+        if (raised && t > pc.t0) {
+#pragma unroll 1
+          for (int q = 0; q < kHalf / 32; q += 2) {
+            uint32_t o[16];
+            const uint32_t oa = lanes + kColO + part * (kHalf / 2) + q * 16;
+            tmem_ld<16>(oa, o);
+            tmem_wait();
+            regs_ready<16>(o);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * a);
+            tmem_st<16>(oa, o);
+            tmem_ld<16>(oa + 16, o);
+            tmem_wait();
+            regs_ready<16>(o);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * a);
+            tmem_st<16>(oa + 16, o);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(p_row + ((part * 4 + c) ^ (r_id & 7)) * 16) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        // a draft's row that only some rows see must not reach the others as
+        // 0 · NaN: where it is not finite it becomes zero (the rows that see it
+        // have it in their sums already)
+        if (pc.mixed && pc.nkeys < (t + 1) * kKeys) {
+          const int sl = tiles % kVs;
+          if (!(ok = waits.warp(&ms.v_full[sl], (tiles / kVs) & 1))) break;
+          const int id = threadIdx.x - kFirstSoft * 32, key = id >> 2;
+          if (t * kKeys + key >= pc.nkeys) {               // (a key past the last draft is zeros)
+            uint4* x = reinterpret_cast<uint4*>(smem + sl * kV + (id & 3) * kChunk + key * 128);
+            bool wild = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t e[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) wild |= (e[i] & 0x7F80u) == 0x7F80u || (e[i] & 0x7F800000u) == 0x7F800000u;
+            }
+            if (wild)
+              for (int j = 0; j < 8; ++j) x[j] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_full);
+      }
+      if (!ok) break;
+      // ---- the next piece's queries, under the last product
+      const int nb = pb ^ 1;
+      if (!(ok = waits.warp(&ms.piece_full[nb], ((pieces + 1) >> 1) & 1))) break;
+      if (ms.piece[nb].t0 != ms.piece[nb].t1) load_q(ms.piece[nb]);
+      // ---- the sum over all keys, and this thread's 128 outputs
+      ms.sum[part][r_id] = l;
+      bar_named(1 + quad, 64);
+      const float z = ms.sum[0][r_id] + ms.sum[1][r_id];
+      const bool whole = pc.slot < 0, have = r_id < pc.rows;
+      float* slot = whole ? nullptr : part_slot(p, blockIdx.x, pc.slot);
+      if (part == 0) {
+        if (!whole) {
+          slot[kRows * kHalf + r_id] = m;
+          slot[kRows * kHalf + kRows + r_id] = z;
+        } else if (p.lse && half == 0 && have) {
+          p.lse[pc.row0 + r_id] = lse_of(m, z);
+        }
+      }
+      const float inv = whole ? (z == 0.f ? 0.f : 1.f / z) : 1.f;
+      if (!(ok = waits.warp(&ms.o_full, pieces & 1))) break;
+      tc_fence_after();
+      const int64_t at = (pc.row0 + r_id) * kLat + half * kHalf + part * (kHalf / 2);
+#pragma unroll 1
+      for (int q = 0; q < kHalf / 2; q += 16) {
+        uint32_t o[16];
+        tmem_ld<16>(lanes + kColO + part * (kHalf / 2) + q, o);
+        tmem_wait();
+        regs_ready<16>(o);
+        float x[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(o[c]) * inv;
+        if (!whole || !p.out_bf16) {
+          float* dst = whole ? static_cast<float*>(p.out) + at + q : slot + r_id * kHalf + part * (kHalf / 2) + q;
+          if (have) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+          }
+        } else if (have) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + q);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            dst[c] = make_uint4(bf_pack(x[8 * c], x[8 * c + 1]), bf_pack(x[8 * c + 2], x[8 * c + 3]),
+                                bf_pack(x[8 * c + 4], x[8 * c + 5]), bf_pack(x[8 * c + 6], x[8 * c + 7]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ms.o_free);
+        mbar_arrive(&ms.piece_empty[pb]);
+      }
+      ++pieces;
+    }
+  }
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+namespace tree {
+
+int launch_tree_mla_wide(const CUtensorMap& tmap_q, const TreeParams& p, int ctas, cudaStream_t stream) {
+  if (const int r = ensure_smem_limit(reinterpret_cast<const void*>(tree_mla_wide_kernel), kSmem)) return r;
+  tree_mla_wide_kernel<<<static_cast<unsigned>(ctas), kThreads, kSmem, stream>>>(tmap_q, p);
+  return check_launch();
+}
+
+}  // namespace tree
+}  // namespace idx
