@@ -34,6 +34,8 @@
 //              stands behind lse adds the weights before that rounding, in fp32.
 // Every wait is bounded; a CTA that gives up raises IDX_DEV_ERR_TIMEOUT, waits for
 // its copies and MMAs, frees TMEM and returns.
+#include <algorithm>
+
 #include "tree_mla.cuh"
 
 namespace idx {
@@ -106,8 +108,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc<N>& ms = *reinterpret_cast<Misc<N>*>(smem + C::kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = blockIdx.x / p.team, rank = blockIdx.x % p.team;
-  const Waits waits{p.budget_ns, &ms.abort_flag, p.err};
+  const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
+  const Waits waits{p.polls, &ms.abort_flag, p.err};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kPairs; ++i) {
@@ -128,12 +130,12 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     tma_prefetch_desc(&tmap_q);
   }
   if (warp == 1) tmem_alloc(&ms.tmem, C::kTmemCols);
-  const Share share = find_share<kTile, C::kThreads>(p, ms, team);
+  const Share share = find_share<N, kTile, C::kThreads>(p, ms, team);
   const uint32_t tmem = ms.tmem;
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp == 0) {
-    plan<N, kTile>(p, ms, share, rank, waits, [&](int row0) {
+    plan<N, kTile, false>(p, ms, share, rank, waits, [&](int row0) {
       mbar_arrive_expect_tx(&ms.q_full, 9 * N * 128);
       for (int c = 0; c < 9; ++c)
         tma_box(smem_base + C::kOffQ + c * N * 128, &tmap_q, smem_u32(&ms.q_full), c * 64, row0);
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     while (true) {
       const int pb = pieces & 1;
       if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
-      const int t0 = ms.piece[pb].t0, t1 = ms.piece[pb].t1;
+      const int t0 = __shfl_sync(0xFFFFFFFFu, ms.piece[pb].t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, ms.piece[pb].t1, 0);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
       if (t0 == t1) break;
@@ -241,8 +243,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     int pairs = 0, ropes = 0, tiles = 0;
     bool ok = true;
     while (ok) {
-      const int par = tiles & 1;
-      if (!waits.warp(&ms.tile_full[par], (tiles >> 1) & 1) || ms.last[par]) break;
+      const int par = tiles % kAhead;
+      if (!waits.nap(&ms.tile_full[par], (tiles / kAhead) & 1) || ms.last[par]) break;
       int row[kRuns], rope_row[kRopeRuns];                 // the last run of some warps is past the tile
 #pragma unroll
       for (int j = 0; j < kRuns; ++j) row[j] = ms.row[par][min(key0 + kStep * j, kTile - 1)];
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       if (lane == 0) mbar_arrive(&ms.tile_read[par]);
       for (int u = 0; u < 4; ++u) {
         const int sl = pairs % C::kPairs;
-        if (pairs >= C::kPairs && !(ok = waits.warp(&ms.pair_empty[sl], (pairs / C::kPairs - 1) & 1))) break;
+        if (pairs >= C::kPairs && !(ok = waits.nap(&ms.pair_empty[sl], (pairs / C::kPairs - 1) & 1))) break;
         const uint32_t to = to_pair + sl * kPair;
         const uint8_t* src = from + u * 256 + piece * 16;
         const uint32_t to_odd = to ^ 64;
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       }
       if (!ok) break;
       const int sl = ropes % C::kRopes;
-      if (ropes >= C::kRopes && !(ok = waits.warp(&ms.rope_empty[sl], (ropes / C::kRopes - 1) & 1))) break;
+      if (ropes >= C::kRopes && !(ok = waits.nap(&ms.rope_empty[sl], (ropes / C::kRopes - 1) & 1))) break;
       const uint32_t to = to_rope + sl * kChunk;
       const uint8_t* src = from + 2 * kLat + (lane & 7) * 16;
 #pragma unroll
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     int tiles = 0, pieces = 0, pairs = 0;
     while (true) {
       const int pb = pieces & 1;
-      if (!(ok = waits.warp(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
+      if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
       const Piece pc = ms.piece[pb];
       if (pc.t0 == pc.t1) break;
       float m = -INFINITY;                                 // reference maximum of column my_col, log2 units
@@ -302,13 +304,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       for (int c = 0; c < NC; ++c) l[c] = 0.f;
       ms.m[sw][my_col] = kNone;
       for (int t = pc.t0; t < pc.t1; ++t, ++tiles, pairs += 4) {
-        if (!(ok = waits.warp(&ms.tile_full[tiles & 1], (tiles >> 1) & 1))) break;
-        const int kind = ms.kind[tiles & 1][key];
+        if (!(ok = waits(&ms.tile_full[tiles % kAhead], (tiles / kAhead) & 1))) break;
+        const int kind = ms.kind[tiles % kAhead][key];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.tile_read[tiles & 1]);
+        if (lane == 0) mbar_arrive(&ms.tile_read[tiles % kAhead]);
         const bool all_seen = __all_sync(0xFFFFFFFFu, kind == 1);
         const bool drafts = __any_sync(0xFFFFFFFFu, kind >= 2);
-        if (!(ok = waits.warp(&ms.s_full, tiles & 1))) break;
+        if (!(ok = waits(&ms.s_full, tiles & 1))) break;
         tc_fence_after();
         uint32_t r[NC];
         tmem_ld<NC>(s_addr, r);
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         // it have it in their weights already)
         if (pc.mixed && drafts && part_id == 0) {
           for (int u = 0; u < 4 && ok; ++u)
-            ok = waits.warp(&ms.pair_full[(pairs + u) % C::kPairs], ((pairs + u) / C::kPairs) & 1);
+            ok = waits(&ms.pair_full[(pairs + u) % C::kPairs], ((pairs + u) / C::kPairs) & 1);
           if (!ok) break;
           if (kind >= 2) {
             bool wild = false;
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         }
       }
       __syncwarp();
-      if (!(ok = waits.warp(&ms.o_full, pieces & 1))) break;
+      if (!(ok = waits(&ms.o_full, pieces & 1))) break;
       tc_fence_after();
 #pragma unroll 1
       for (int blk = 0; blk < 4; ++blk) {
@@ -492,9 +494,9 @@ __global__ void __launch_bounds__(kJoinGroups * 128) tree_mla_join_kernel(const 
   const int group = threadIdx.x >> 7, id = threadIdx.x & 127;
   const int D = kLat / p.halves;               // output features per slot row
   const int sub = id / (D / 4), d = id % (D / 4);
-  const int team = blockIdx.x / p.team, rank = blockIdx.x % p.team;
+  const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
   auto slot = [&](int i) {                     // piece 0 is this team's slot 1, the others the next teams' slot 0
-    return part_slot(p, static_cast<int64_t>(team + i) * p.team + rank, i == 0 ? 1 : 0);
+    return part_slot(p, static_cast<int64_t>(team + i) * p.halves + rank, i == 0 ? 1 : 0);
   };
   for (int c0 = blockIdx.y * p.halves; c0 < cut.rows; c0 += kJoinY * p.halves) {
     const int c = min(c0 + sub, p.M - 1);
@@ -531,14 +533,14 @@ __global__ void __launch_bounds__(kJoinGroups * 128) tree_mla_join_kernel(const 
         z += sums[g][sub];
       }
       const float inv = z == 0.f ? 0.f : 1.f / z;
-      const int64_t at = (cut.row0 + c) * kLat + (rank % p.halves) * D + d * 4;
+      const int64_t at = (cut.row0 + c) * kLat + rank * D + d * 4;
       if (p.out_bf16)
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
             make_uint2(bf_pack(o.x * inv, o.y * inv), bf_pack(o.z * inv, o.w * inv));
       else
         *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      if (p.lse && d == 0 && rank % p.halves == 0) p.lse[cut.row0 + c] = lse_of(top, z);
+      if (p.lse && d == 0 && rank == 0) p.lse[cut.row0 + c] = lse_of(top, z);
     }
     __syncthreads();
   }
@@ -549,9 +551,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // How a call's rows and tiles are dealt.  Rows that share keys: up to 64 go to the
 // transposed kernel above with the fewest columns that hold them (16, 32, 64);
 // more to the wide kernel (tree_mla_wide.cu) in groups of 128, two CTAs each.
-constexpr int kMaxGroups = 8;                 // row groups per team
 struct Plan {
-  int M, halves, team, blocks, teams, whole;
+  int M, halves, teams, whole;
   size_t part_bytes, ws;
 };
 Plan plan_for(int n, int H, int max_len, int k, int sms) {
@@ -559,13 +560,10 @@ Plan plan_for(int n, int H, int max_len, int k, int sms) {
   const int64_t rows = k ? H : static_cast<int64_t>(n) * H;
   pl.M = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   pl.halves = pl.M == 128 ? 2 : 1;
-  const int64_t groups = (rows + pl.M - 1) / pl.M;
-  pl.blocks = static_cast<int>((groups + kMaxGroups - 1) / kMaxGroups);
-  pl.team = static_cast<int>((groups + pl.blocks - 1) / pl.blocks) * pl.halves;
-  pl.teams = sms / pl.team > 0 ? sms / pl.team : 1;
+  pl.teams = sms / pl.halves > 0 ? sms / pl.halves : 1;
   const int64_t keys = k ? static_cast<int64_t>(k) + n : max_len;
   pl.whole = keys <= kMinShare || pl.teams == 1;
-  const size_t ctas = static_cast<size_t>(pl.teams) * pl.team;
+  const size_t ctas = static_cast<size_t>(pl.teams) * pl.halves;
   pl.part_bytes = ctas * 2 * pl.M * (kLat / pl.halves + 2) * sizeof(float);
   pl.ws = pl.whole ? 0 : pl.part_bytes + ctas * sizeof(Cut);
   return pl;
@@ -615,7 +613,7 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
   const Plan pl = plan_for(n, H, max_len, k, num_sms());
   if (pl.ws > 0 && !ws) return IDX_ERR_NULL;
   if (ws_bytes < pl.ws) return IDX_ERR_SCRATCH;
-  const int ctas = pl.teams * pl.team;
+  const int ctas = pl.teams * pl.halves;
   CUtensorMap tq;
   if (!make_tmap_2d_bf16_sw128(&tq, q, kRow, static_cast<uint64_t>(rows) * H, static_cast<uint32_t>(pl.M)))
     return IDX_ERR_UNSUPPORTED;
@@ -646,13 +644,11 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
   p.lse = lse;
   p.M = pl.M;
   p.halves = pl.halves;
-  p.team = pl.team;
-  p.blocks = pl.blocks;
   p.teams = pl.teams;
   p.whole = pl.whole;
   p.part = static_cast<float*>(ws);
   p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(ws) + pl.part_bytes);
-  p.budget_ns = debug_state().budget_ns;
+  p.polls = static_cast<uint32_t>(std::min<unsigned long long>(debug_state().budget_ns / 20, 0xFFFFFF00ull));
   p.err = device_error_word();
   if (!p.err) return check_launch();
   auto* s = reinterpret_cast<cudaStream_t>(stream);

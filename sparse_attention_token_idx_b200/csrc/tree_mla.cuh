@@ -2,13 +2,15 @@
 // is dealt to the CTAs, the planner warp that walks a CTA's share, the join of
 // items that shares cut, and inline PTX.
 //
-// Work: an item is a row block of a sequence (of a token, where each token has
-// its own selection) with all keys that it sees, in tiles of KT keys.  The tiles
-// of all items are numbered through and dealt in equal contiguous shares to teams
-// of CTAs, one persistent CTA per SM; the CTAs of a team walk the same tiles with
-// different rows or output columns, so a tile comes from HBM once and from L2
-// after that.  An item that a share's end cuts leaves partial (O, maximum, sum)
-// in the workspace, and tree_mla_join adds them in a fixed order.
+// Work: an item is a group of M rows of a sequence (of a token, where each token
+// has its own selection) with all keys that they see, in tiles of KT keys.  The
+// tiles of all items are numbered through and dealt in equal contiguous shares to
+// teams of CTAs, one persistent CTA per SM (a team is one CTA, or the two that
+// share a row's output columns); so ragged lengths and counts cost nothing.
+// Groups of one sequence lie side by side in that order: their teams read its
+// rows at about the same time, from L2 after the first.  An item that a share's
+// end cuts leaves partial (O, maximum, sum) in the workspace, and
+// tree_mla_join_kernel adds them in a fixed order.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -24,6 +26,7 @@ namespace tree {
 
 constexpr int kLat = 512, kRow = 576;
 constexpr int kMinShare = 256;                // keys per share below which work is not split further
+constexpr int kAhead = 4;                     // tiles that the planner may be ahead of its readers
 constexpr float kRaise = 8.f;                 // log2 margin of the reference maximum
 constexpr float kNone = -3.0e38f;             // stands for a reference maximum of −inf: any score passes it
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -57,12 +60,11 @@ struct TreeParams {
   void* out;
   int out_bf16;
   float* lse;
-  int M, halves;                              // rows per CTA; CTAs that share the output columns of a row
-  int team, blocks;                           // CTAs per team, row blocks (of a team's rows) per token set
+  int M, halves;                              // rows per CTA; CTAs (a team) that share the output columns of a row
   int teams, whole;                           // whole: items are not cut
   float* part;                                // [CTA][2] partial slots: M · (512 / halves) outputs, M maxima, M sums
   Cut* cuts;                                  // [CTA]
-  unsigned long long budget_ns;
+  uint32_t polls;                             // bound of every wait
   unsigned int* err;
 };
 
@@ -74,15 +76,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
   return p != 0;
 }
-// mbar_wait that polls 256 times before it looks at the clock: a read of the
-// global timer takes about 1 000 cycles, which every wait that does not succeed
-// at once would add to its hand-off
-__device__ __forceinline__ bool mbar_wait_polling(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
-                                                  volatile int* abort_flag, unsigned int* err) {
-  for (int i = 0; i < 256; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, budget_ns, abort_flag, err);
-}
 // 16 bytes into shared memory, zeros where bytes = 0; cp_async_arrive makes the
 // barrier count this thread once its copies so far have landed
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -90,6 +83,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 }
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
@@ -162,25 +158,34 @@ __device__ __forceinline__ bool bar_named_any(int id, int count, bool v) {
       : "memory");
   return r != 0;
 }
-// every lane polls, or lane 0 for its warp; false once the CTA has given up
+// A warp's wait for a phase of an mbarrier, bounded by a number of polls (at least
+// 20 ns each); false once this CTA has given up.  Short and without the global
+// timer, whose read takes about 1 000 cycles: a wait that succeeds at once costs
+// some 60 cycles instead of 300, and there are a dozen per tile on the critical
+// path.  The vote makes the answer uniform for the compiler, so that what the MMA
+// issue computes stays in uniform registers.  nap: about 50 ns between polls,
+// where nobody waits for this warp, so that the shared-memory queue stays free.
 struct Waits {
-  uint64_t budget;
+  uint32_t polls;
   volatile int* abort_flag;
   unsigned int* err;
-  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    return mbar_wait_polling(bar, parity, budget, abort_flag, err);
+  template <bool kNap>
+  __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) const {
+    for (uint32_t i = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++i) {
+      if ((i & 63) == 63 && __any_sync(0xFFFFFFFFu, *abort_flag || i > polls)) {
+        if (!*abort_flag) raise_error(err, IDX_DEV_ERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+      if (kNap) __nanosleep(40);
+    }
+    return true;
   }
-  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
-    int w = 1;
-    if ((threadIdx.x & 31) == 0) w = mbar_wait_polling(bar, parity, budget, abort_flag, err) ? 1 : 0;
-    w = __shfl_sync(0xFFFFFFFFu, w, 0);
-    __syncwarp();
-    return w != 0;
-  }
-  // during teardown: whatever happened before, wait for what is in flight
+  __device__ __forceinline__ bool nap(uint64_t* bar, uint32_t parity) const { return poll<true>(bar, parity); }
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const { return poll<false>(bar, parity); }
+  // during teardown: whatever happened before, wait (the whole warp) for what is in flight
   __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
-    int dummy = 0;
-    mbar_wait(bar, parity, budget, &dummy, err);
+    for (uint32_t i = 0; i <= polls && !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++i) {}
   }
 };
 
@@ -227,9 +232,9 @@ __device__ __forceinline__ void regs_ready(uint32_t* r) {
 
 // ------------------------------------------------------------------ work
 struct Seq {
-  int len, cnt, ctx, items, tiles;            // items: row blocks to serve; tiles per item
+  int len, cnt, ctx, groups, items, tiles;    // row groups (of a token, where each has its selection); tiles per item
 };
-template <int KT>
+template <int M, int KT>
 __device__ __forceinline__ Seq seq_info(const TreeParams& p, int b, bool report) {
   Seq s;
   s.cnt = p.counts ? __ldg(p.counts + b) : p.n;
@@ -239,7 +244,8 @@ __device__ __forceinline__ Seq seq_info(const TreeParams& p, int b, bool report)
     s.cnt = s.len = 0;
   }
   s.ctx = s.len - s.cnt;
-  s.items = p.indices ? s.cnt * p.blocks : s.cnt > 0 ? p.blocks : 0;
+  s.groups = static_cast<int>(((p.indices ? 1 : s.cnt) * static_cast<int64_t>(p.H) + M - 1) / M);
+  s.items = p.indices ? s.cnt * s.groups : s.groups;
   s.tiles = (static_cast<int>(p.indices ? p.k + s.cnt : s.len) + KT - 1) / KT;
   return s;
 }
@@ -256,21 +262,23 @@ __device__ __forceinline__ uint64_t draft_mask(const TreeParams& p, int b, int i
 template <int M, int KT, int kWarps>
 struct PlanState {
   uint64_t mask[2][M];                        // per piece parity: drafts each row sees
-  alignas(16) uint8_t kind[2][KT];            // per tile parity and key: 0 unseen, 1 context, 2 + j draft j
-  alignas(16) int row[2][KT];                 // per tile parity: cache rows of the keys, −1: none
-  int last[2];                                // per tile parity: no tile, the list has ended
+  alignas(16) uint8_t kind[kAhead][KT];       // per tile (mod kAhead) and key: 0 unseen, 1 context, 2 + j draft j
+  alignas(16) int row[kAhead][KT];            // cache rows of the keys, −1: none
+  int last[kAhead];                           // no tile: the list has ended
   Piece piece[2];
   long long scan[kWarps];
   long long start_off;
   int start_b;
   int abort_flag;
   uint32_t tmem;
-  uint64_t tile_full[2], tile_read[2], piece_full[2], piece_empty[2], q_full, q_empty;
+  uint64_t tile_full[kAhead], tile_read[kAhead], piece_full[2], piece_empty[2], q_full, q_empty;
 
   __device__ void init(int B, int tile_readers, int piece_readers) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       mbar_init(&tile_full[i], 1);
       mbar_init(&tile_read[i], tile_readers);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&piece_full[i], 1);
       mbar_init(&piece_empty[i], piece_readers);
     }
@@ -288,14 +296,14 @@ struct Share {
 // Where this team's share lies: every thread of the CTA adds up a run of
 // sequences, then the one whose run holds the share's begin looks for it.  Two
 // CTA barriers; what was written before the first is visible after it.
-template <int KT, int kThreads, class State>
+template <int M, int KT, int kThreads, class State>
 __device__ __forceinline__ Share find_share(const TreeParams& p, State& ms, int team) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
-    const Seq s = seq_info<KT>(p, b, blockIdx.x == 0);
+    const Seq s = seq_info<M, KT>(p, b, blockIdx.x == 0);
     mine += static_cast<long long>(s.items) * (p.whole ? 1 : s.tiles);
   }
   long long incl = mine;
@@ -320,7 +328,7 @@ __device__ __forceinline__ Share find_share(const TreeParams& p, State& ms, int 
   if (sh.begin < sh.end && before + incl - mine <= sh.begin && sh.begin < before + incl) {
     long long at = before + incl - mine;
     for (int b = b_lo; b < b_hi; ++b) {
-      const Seq s = seq_info<KT>(p, b, false);
+      const Seq s = seq_info<M, KT>(p, b, false);
       const long long w = static_cast<long long>(s.items) * (p.whole ? 1 : s.tiles);
       if (sh.begin < at + w) {
         ms.start_b = b;
@@ -337,7 +345,7 @@ __device__ __forceinline__ Share find_share(const TreeParams& p, State& ms, int 
 // The planner warp: walks the share, publishes each piece (tile range, what its
 // rows see of the drafts) and each tile (cache rows of its keys), and has the
 // piece's queries loaded: load_q(row0) issues them on ms.q_full.
-template <int M, int KT, class State, class LoadQ>
+template <int M, int KT, bool kPrefetch, class State, class LoadQ>
 __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share& sh, int rank, const Waits& waits,
                                      LoadQ load_q) {
   constexpr int E = KT / 32;                  // keys per lane
@@ -349,12 +357,12 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
   long long off = ms.start_off;
   Cut cut{0, 0, 0};
   Seq s{};
-  if (b < p.B) s = seq_info<KT>(p, b, false);
+  if (b < p.B) s = seq_info<M, KT>(p, b, false);
   while (ok && cur < sh.end) {
     const int weight = p.whole ? 1 : s.tiles;
     if (off >= static_cast<long long>(s.items) * weight) {
       if (++b >= p.B) break;
-      s = seq_info<KT>(p, b, false);
+      s = seq_info<M, KT>(p, b, false);
       off = 0;
       continue;
     }
@@ -366,11 +374,10 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
     cur += step;
     // this CTA's rows: M flattened (token, head) rows of the sequence, or M heads
     // of one token where each token has its selection
-    const int tok = p.indices ? item / p.blocks : 0;
-    const int blk = p.indices ? item % p.blocks : item;
-    const int64_t lo = (static_cast<int64_t>(blk) * (p.team / p.halves) + rank / p.halves) * M;
+    const int tok = p.indices ? item / s.groups : 0;
+    const int64_t lo = static_cast<int64_t>(p.indices ? item % s.groups : item) * M;
     const int64_t have = p.indices ? p.H : static_cast<int64_t>(s.cnt) * p.H;
-    const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(M), have - lo)));
+    const int rows = static_cast<int>(min(static_cast<int64_t>(M), have - lo));
     const int64_t row0 = (static_cast<int64_t>(b) * p.n + tok) * p.H + lo;
     const int slot = t0 == 0 && t1 == s.tiles ? -1 : t0 == 0 ? 1 : 0;
     if (slot == 1) {
@@ -378,10 +385,9 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
       cut.rows = rows;
       cut.pieces = static_cast<int>((s.tiles - t1 + sh.size - 1) / sh.size);
     }
-    if (rows == 0) continue;                  // the team has more rows than this sequence
     const int nkeys = p.indices ? p.k : s.ctx;
     const int pb = pieces & 1;
-    if (pieces >= 2 && !(ok = waits.warp(&ms.piece_empty[pb], ((pieces >> 1) - 1) & 1))) break;
+    if (pieces >= 2 && !(ok = waits.nap(&ms.piece_empty[pb], ((pieces >> 1) - 1) & 1))) break;
     uint64_t any = 0;
     for (int c = lane; c < M; c += 32) {
       const uint64_t m = c < rows ? draft_mask(p, b, p.indices ? tok : static_cast<int>((lo + c) / p.H), s.cnt) : 0;
@@ -453,9 +459,23 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
           pos_far[e] = position(t + 2, e);
         }
       }
-      const int par = tiles & 1;
-      // free once the copies and the softmax have read what it said two tiles ago
-      if (tiles >= 2 && !(ok = waits.warp(&ms.tile_read[par], ((tiles >> 1) - 1) & 1))) break;
+      if (kPrefetch && lane % p.halves == rank) {
+        // into L2, ahead of the copies: each CTA of the team asks for its share of the rows
+        const uint8_t* at = reinterpret_cast<const uint8_t*>(p.cache);
+        bool run = row[0] >= 0;
+#pragma unroll
+        for (int e = 1; e < E; ++e) run &= row[e] == row[0] + e;
+        if (run) {
+          prefetch_l2(at + static_cast<int64_t>(row[0]) * (2 * kRow), E * 2 * kRow);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (row[e] >= 0) prefetch_l2(at + static_cast<int64_t>(row[e]) * (2 * kRow), 2 * kRow);
+        }
+      }
+      const int par = tiles % kAhead;
+      // free once the copies and the softmax have read what it said kAhead tiles ago
+      if (tiles >= kAhead && !(ok = waits.nap(&ms.tile_read[par], (tiles / kAhead - 1) & 1))) break;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         ms.kind[par][E * lane + e] = static_cast<uint8_t>(kinds >> (8 * e));
@@ -466,7 +486,7 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
       if (lane == 0) mbar_arrive(&ms.tile_full[par]);
       ++tiles;
       if (t == t0) {                          // its queries, once the last piece's are no longer read
-        if (pieces >= 1 && !(ok = waits.warp(&ms.q_empty, (pieces - 1) & 1))) break;
+        if (pieces >= 1 && !(ok = waits.nap(&ms.q_empty, (pieces - 1) & 1))) break;
         if (elect_one()) load_q(static_cast<int>(row0));
         __syncwarp();
         ++pieces;
@@ -476,21 +496,20 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
   // the end of the list
   if (ok) {
     const int pb = pieces & 1;
-    if (pieces >= 2) ok = waits.warp(&ms.piece_empty[pb], ((pieces >> 1) - 1) & 1);
+    if (pieces >= 2) ok = waits.nap(&ms.piece_empty[pb], ((pieces >> 1) - 1) & 1);
     if (ok && lane == 0) {
       ms.piece[pb].t0 = ms.piece[pb].t1 = 0;
       mbar_arrive(&ms.piece_full[pb]);
     }
-    const int par = tiles & 1;
-    if (ok && tiles >= 2) ok = waits.warp(&ms.tile_read[par], ((tiles >> 1) - 1) & 1);
+    const int par = tiles % kAhead;
+    if (ok && tiles >= kAhead) ok = waits.nap(&ms.tile_read[par], (tiles / kAhead - 1) & 1);
     if (ok && lane == 0) {
       ms.last[par] = 1;
       mbar_arrive(&ms.tile_full[par]);
     }
   }
   if (!p.whole && lane == 0) p.cuts[blockIdx.x] = cut;
-  if (lane == 0 && pieces) waits.drain(&ms.q_full, (pieces - 1) & 1);   // landed before the memory goes
-  __syncwarp();
+  if (pieces) waits.drain(&ms.q_full, (pieces - 1) & 1);   // landed before the memory goes
 }
 
 __device__ __forceinline__ float lse_of(float m, float z) {    // m in log2 units

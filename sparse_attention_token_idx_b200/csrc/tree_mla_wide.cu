@@ -56,7 +56,7 @@ static_assert(kColS + kKeys <= kColO, "TMEM columns");
 
 struct WideState : PlanState<kRows, kKeys, kThreads / 32> {
   float top[2][kRows], sum[2][kRows];         // per half of the keys
-  uint64_t v_full[kVs], v_empty[kVs], x_full[kXs], x_empty[kXs];
+  uint64_t v_full[kVs], v_empty[kVs], x_full[2], x_empty[kXs];
   uint64_t q_ready, s_full, s_free, p_full, p_free, o_full, o_free, drain_bar;
 };
 constexpr int kSmem = 1024 + kOffMisc + static_cast<int>(sizeof(WideState));
@@ -74,19 +74,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   WideState& ms = *reinterpret_cast<WideState*>(smem + kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = blockIdx.x / p.team, rank = blockIdx.x % p.team;
-  const int half = rank & 1;
-  const Waits waits{p.budget_ns, &ms.abort_flag, p.err};
+  const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
+  const int half = rank;
+  const Waits waits{p.polls, &ms.abort_flag, p.err};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kVs; ++i) {
       mbar_init(&ms.v_full[i], kCopyWarps * 32);
       mbar_init(&ms.v_empty[i], 1);
     }
-    for (int i = 0; i < kXs; ++i) {
-      mbar_init(&ms.x_full[i], kCopyWarps * 32);
-      mbar_init(&ms.x_empty[i], 1);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(&ms.x_full[i], kCopyWarps * 32);
+    for (int i = 0; i < kXs; ++i) mbar_init(&ms.x_empty[i], 1);
     mbar_init(&ms.q_ready, kSoftWarps);
     mbar_init(&ms.s_full, 1);
     mbar_init(&ms.s_free, kSoftWarps);
@@ -100,12 +98,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmap_q);
   }
   if (warp == 1) tmem_alloc(&ms.tmem, 512);
-  const Share share = find_share<kKeys, kThreads>(p, ms, team);
+  const Share share = find_share<kRows, kKeys, kThreads>(p, ms, team);
   const uint32_t tmem = ms.tmem;
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp == 0) {
-    plan<kRows, kKeys>(p, ms, share, rank, waits, [&](int row0) {
+    plan<kRows, kKeys, true>(p, ms, share, rank, waits, [&](int row0) {
       mbar_arrive_expect_tx(&ms.q_full, 3 * kQChunk);
       for (int c = 0; c < 3; ++c)
         tma_box(smem_base + kOffQ + c * kQChunk, &tmap_q, smem_u32(&ms.q_full), feature_chunk(kQTmem + c, half) * 64,
@@ -125,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (true) {
       const int pb = pieces & 1;
       if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
-      const int n = ms.piece[pb].t1 - ms.piece[pb].t0;
+      const int n = __shfl_sync(0xFFFFFFFFu, ms.piece[pb].t1 - ms.piece[pb].t0, 0);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
       if (n == 0) break;
@@ -134,8 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c < n) {
           // S = q · Kᵀ of tile c, once the softmax has read the last S
           if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
-          for (int u = 0; u < 5 && ok; ++u) ok = waits(&ms.x_full[(xs + u) % kXs], ((xs + u) / kXs) & 1);
-          if (!ok) break;
+          if (!(ok = waits(&ms.x_full[tiles & 1], (tiles >> 1) & 1))) break;
           fence_proxy_async_smem();            // the copies wrote through the generic proxy
           tc_fence_after();
           if (elect_one()) {
@@ -211,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int xs = 0, tiles = 0;
     bool ok = true;
     while (ok) {
-      const int par = tiles & 1;
-      if (!waits.warp(&ms.tile_full[par], (tiles >> 1) & 1) || ms.last[par]) break;
+      const int par = tiles % kAhead;
+      if (!waits.nap(&ms.tile_full[par], (tiles / kAhead) & 1) || ms.last[par]) break;
       int row[8], xrow[2];
 #pragma unroll
       for (int j = 0; j < 8; ++j) row[j] = ms.row[par][w + 8 * j];
@@ -222,18 +219,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ms.tile_read[par]);
       for (int u = 0; u < 5; ++u) {
         const int sl = xs % kXs;
-        if (xs >= kXs && !(ok = waits.warp(&ms.x_empty[sl], (xs / kXs - 1) & 1))) break;
+        if (xs >= kXs && !(ok = waits.nap(&ms.x_empty[sl], (xs / kXs - 1) & 1))) break;
         const uint8_t* src = from + feature_chunk(u, half) * 128 + (lane & 7) * 16;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           cp_async16(to_x + sl * kChunk + j * 4096, src + static_cast<int64_t>(max(xrow[j], 0)) * (2 * kRow),
                      xrow[j] >= 0 ? 16 : 0);
-        cp_async_arrive(&ms.x_full[sl]);
         ++xs;
       }
       if (!ok) break;
+      cp_async_arrive(&ms.x_full[tiles & 1]);
       const int sl = tiles % kVs;
-      if (tiles >= kVs && !(ok = waits.warp(&ms.v_empty[sl], (tiles / kVs - 1) & 1))) break;
+      if (tiles >= kVs && !(ok = waits.nap(&ms.v_empty[sl], (tiles / kVs - 1) & 1))) break;
       const uint8_t* src = from + half * 512 + lane * 16;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -274,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.q_ready);
     };
-    ok = waits.warp(&ms.piece_full[0], 0);
+    ok = waits(&ms.piece_full[0], 0);
     if (ok && ms.piece[0].t0 != ms.piece[0].t1) load_q(ms.piece[0]);
     while (ok) {
       const int pb = pieces & 1;
@@ -285,18 +282,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = pc.t0; t < pc.t1; ++t, ++tiles) {
         // what this row sees of the tile's keys: the context, and its drafts (draft
         // j is key nkeys + j)
-        if (!(ok = waits.warp(&ms.tile_full[tiles & 1], (tiles >> 1) & 1))) break;
-        const int k0 = ms.kind[tiles & 1][part * 32 + lane];
+        if (!(ok = waits(&ms.tile_full[tiles % kAhead], (tiles / kAhead) & 1))) break;
+        const int k0 = ms.kind[tiles % kAhead][part * 32 + lane];
         const uint32_t ctx = __ballot_sync(0xFFFFFFFFu, k0 == 1), dr = __ballot_sync(0xFFFFFFFFu, k0 >= 2);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.tile_read[tiles & 1]);
+        if (lane == 0) mbar_arrive(&ms.tile_read[tiles % kAhead]);
         uint32_t sees = ctx;
         if (dr) {
           const int sh = pc.nkeys - (t * kKeys + part * 32);   // key of draft 0 in these 32
           const uint64_t at = sh >= 0 ? (sh < 64 ? drafts << sh : 0) : (sh > -64 ? drafts >> -sh : 0);
           sees |= static_cast<uint32_t>(at) & dr;
         }
-        if (!(ok = waits.warp(&ms.s_full, tiles & 1))) break;
+        if (!(ok = waits(&ms.s_full, tiles & 1))) break;
         tc_fence_after();
         uint32_t r[32];
         tmem_ld<16>(lanes + kColS + part * 32, r);
@@ -342,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += p0 + p1;
         }
         // P and O are free once the last product has ended
-        if (tiles >= 1 && !(ok = waits.warp(&ms.p_free, (tiles - 1) & 1))) break;
+        if (tiles >= 1 && !(ok = waits(&ms.p_free, (tiles - 1) & 1))) break;
         tc_fence_after();
         if (raised && t > pc.t0) {
 #pragma unroll 1
@@ -373,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // have it in their sums already)
         if (pc.mixed && pc.nkeys < (t + 1) * kKeys) {
           const int sl = tiles % kVs;
-          if (!(ok = waits.warp(&ms.v_full[sl], (tiles / kVs) & 1))) break;
+          if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
           const int id = threadIdx.x - kFirstSoft * 32, key = id >> 2;
           if (t * kKeys + key >= pc.nkeys) {               // (a key past the last draft is zeros)
             uint4* x = reinterpret_cast<uint4*>(smem + sl * kV + (id & 3) * kChunk + key * 128);
@@ -396,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // ---- the next piece's queries, under the last product
       const int nb = pb ^ 1;
-      if (!(ok = waits.warp(&ms.piece_full[nb], ((pieces + 1) >> 1) & 1))) break;
+      if (!(ok = waits(&ms.piece_full[nb], ((pieces + 1) >> 1) & 1))) break;
       if (ms.piece[nb].t0 != ms.piece[nb].t1) load_q(ms.piece[nb]);
       // ---- the sum over all keys, and this thread's 128 outputs
       ms.sum[part][r_id] = l;
@@ -413,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float inv = whole ? (z == 0.f ? 0.f : 1.f / z) : 1.f;
-      if (!(ok = waits.warp(&ms.o_full, pieces & 1))) break;
+      if (!(ok = waits(&ms.o_full, pieces & 1))) break;
       tc_fence_after();
       const int64_t at = (pc.row0 + r_id) * kLat + half * kHalf + part * (kHalf / 2);
 #pragma unroll 1
