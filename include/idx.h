@@ -422,10 +422,10 @@ enum idx_out_dtype { IDX_OUT_F32 = 0, IDX_OUT_BF16 = 1 };
  *   A row that sees nothing gives out = 0, lse = −inf.  Cache rows that a
  *   sequence does not hold are never read as numbers.
  *   ws / ws_bytes: at least idx_tree_mla_workspace_size(B, n, H, max_len, k)
- *            bytes, 16-byte aligned (may be NULL where that is 0).  It holds
+ *            bytes, 32-byte aligned (may be NULL where that is 0).  It holds
  *            partial results inside the call: calls (or captured graphs) that may
  *            run at the same time need one each.
- * q, cache, out, ws: 16-byte aligned; tree_mask 8.  Scores and sums in fp32.
+ * q, cache: 16-byte aligned; out, ws 32; tree_mask 8.  Scores and sums in fp32.
  * Errors: IDX_ERR_SHAPE, IDX_ERR_NULL, IDX_ERR_ALIGN, IDX_ERR_FMT (out_dtype),
  * IDX_ERR_SCRATCH.  counts[b] outside [0, n], lengths[b] < counts[b] or
  * lengths[b] > max_len raise IDX_DEV_ERR_LENGTH and leave the sequence's outputs as

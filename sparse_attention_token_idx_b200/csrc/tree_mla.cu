@@ -34,8 +34,6 @@
 //              stands behind lse adds the weights before that rounding, in fp32.
 // Every wait is bounded; a CTA that gives up raises IDX_DEV_ERR_TIMEOUT, waits for
 // its copies and MMAs, frees TMEM and returns.
-#include <algorithm>
-
 #include "tree_mla.cuh"
 
 namespace idx {
@@ -109,7 +107,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
   Misc<N>& ms = *reinterpret_cast<Misc<N>*>(smem + C::kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
-  const Waits waits{p.polls, &ms.abort_flag, p.err};
+  const Waits waits{p.budget_ns, &ms.abort_flag, p.err};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kPairs; ++i) {
@@ -155,7 +153,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     while (true) {
       const int pb = pieces & 1;
       if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
-      const int t0 = __shfl_sync(0xFFFFFFFFu, ms.piece[pb].t0, 0), t1 = __shfl_sync(0xFFFFFFFFu, ms.piece[pb].t1, 0);
+      const int t0 = __reduce_max_sync(0xFFFFFFFFu, ms.piece[pb].t0), t1 = __reduce_max_sync(0xFFFFFFFFu, ms.piece[pb].t1);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
       if (t0 == t1) break;
@@ -482,56 +480,67 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
 }
 
 // Joins the pieces of the items that shares cut: CTA (x, y) takes every kJoinY-th
-// row (or run of rows) of the item that begins in CTA x's share and goes on in the
-// next teams'.  Four groups of 128 threads walk every fourth piece, a thread ↔ four
-// output features of a row; their sums are added in a fixed order.
-constexpr int kJoinGroups = 4, kJoinY = 8;
-__global__ void __launch_bounds__(kJoinGroups * 128) tree_mla_join_kernel(const TreeParams p) {
-  __shared__ float4 acc[kJoinGroups][128];
-  __shared__ float sums[kJoinGroups][2];
+// run of outputs of the item that begins in CTA x's share and goes on in the next
+// teams'.  A thread ↔ four output features of a row, walking the pieces with a
+// running maximum; many pieces (one long sequence) are split over four threads,
+// whose results are added in a fixed order.  Reads what the pieces wrote, from L2.
+constexpr int kJoinThreads = 256, kJoinY = 16;
+__global__ void __launch_bounds__(kJoinThreads) tree_mla_join_kernel(const TreeParams p) {
+  __shared__ float4 acc[kJoinThreads];
+  __shared__ float2 stat[kJoinThreads];
   const Cut cut = p.cuts[blockIdx.x];
   if (!cut.pieces) return;
-  const int group = threadIdx.x >> 7, id = threadIdx.x & 127;
-  const int D = kLat / p.halves;               // output features per slot row
-  const int sub = id / (D / 4), d = id % (D / 4);
+  const int D = kLat / p.halves, D4 = D / 4;   // output features per slot row
+  const int split = cut.pieces >= 8 ? 4 : 1, width = kJoinThreads / split;
+  const int group = threadIdx.x / width, id = threadIdx.x % width;
   const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
-  auto slot = [&](int i) {                     // piece 0 is this team's slot 1, the others the next teams' slot 0
-    return part_slot(p, static_cast<int64_t>(team + i) * p.halves + rank, i == 0 ? 1 : 0);
-  };
-  for (int c0 = blockIdx.y * p.halves; c0 < cut.rows; c0 += kJoinY * p.halves) {
-    const int c = min(c0 + sub, p.M - 1);
+  const int64_t stride = static_cast<int64_t>(p.halves) * 2 * p.M * (D + 2);
+  const float* next = part_slot(p, static_cast<int64_t>(team) * p.halves + rank, 0);   // slot 0 of this team
+  const float* first = part_slot(p, static_cast<int64_t>(team) * p.halves + rank, 1);
+  for (int e0 = blockIdx.y * width; e0 < cut.rows * D4; e0 += kJoinY * width) {
+    const int e = min(e0 + id, cut.rows * D4 - 1), c = e / D4, d = e % D4;
     const int at_m = p.M * D + c, at_z = at_m + p.M;
-    float top = -INFINITY;
-    for (int i = 0; i <= cut.pieces; ++i) top = fmaxf(top, slot(i)[at_m]);
-    const float base = top == -INFINITY ? 0.f : top;
+    float top = -INFINITY, z = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float z = 0.f;
 #pragma unroll 4
-    for (int i = group; i <= cut.pieces; i += kJoinGroups) {
-      const float* s = slot(i);
-      const float w = ex2(s[at_m] - base);
+    for (int i = group; i <= cut.pieces; i += split) {
+      const float* s = i == 0 ? first : next + i * stride;   // piece 0: this team's slot 1; then the next teams' slot 0
+      const float m = s[at_m], zi = s[at_z];
       const float4 x = *reinterpret_cast<const float4*>(s + c * D + d * 4);
-      o.x += w * x.x;
-      o.y += w * x.y;
-      o.z += w * x.z;
-      o.w += w * x.w;
-      z += w * s[at_z];
+      const float up = fmaxf(top, m), base = up == -INFINITY ? 0.f : up;
+      const float a = ex2(top - base), w = ex2(m - base);
+      o.x = o.x * a + w * x.x;
+      o.y = o.y * a + w * x.y;
+      o.z = o.z * a + w * x.z;
+      o.w = o.w * a + w * x.w;
+      z = z * a + w * zi;
+      top = up;
     }
-    acc[group][id] = o;
-    if (d == 0) sums[group][sub] = z;
-    __syncthreads();
-    if (group == 0 && c0 + sub < cut.rows) {
-      z = 0.f;
-      o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int g = 0; g < kJoinGroups; ++g) {
-        const float4 x = acc[g][id];
-        o.x += x.x;
-        o.y += x.y;
-        o.z += x.z;
-        o.w += x.w;
-        z += sums[g][sub];
+    if (split > 1) {
+      acc[threadIdx.x] = o;
+      stat[threadIdx.x] = make_float2(top, z);
+      __syncthreads();
+      if (group == 0) {
+        float up = top;
+        for (int g = 1; g < split; ++g) up = fmaxf(up, stat[g * width + id].x);
+        const float base = up == -INFINITY ? 0.f : up;
+        z = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g = 0; g < split; ++g) {
+          const float4 x = acc[g * width + id];
+          const float2 mz = stat[g * width + id];
+          const float w = ex2(mz.x - base);
+          o.x += w * x.x;
+          o.y += w * x.y;
+          o.z += w * x.z;
+          o.w += w * x.w;
+          z += w * mz.y;
+        }
+        top = up;
       }
+      __syncthreads();
+    }
+    if (group == 0 && e0 + id < cut.rows * D4) {
       const float inv = z == 0.f ? 0.f : 1.f / z;
       const int64_t at = (cut.row0 + c) * kLat + rank * D + d * 4;
       if (p.out_bf16)
@@ -542,7 +551,6 @@ __global__ void __launch_bounds__(kJoinGroups * 128) tree_mla_join_kernel(const 
             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
       if (p.lse && d == 0 && rank == 0) p.lse[cut.row0 + c] = lse_of(top, z);
     }
-    __syncthreads();
   }
 }
 
@@ -606,7 +614,7 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
     return IDX_ERR_SHAPE;
   if ((k > 0) != (indices != nullptr)) return indices ? IDX_ERR_K : IDX_ERR_NULL;
   if (!q || !cache || !page_table || !lengths || !out) return IDX_ERR_NULL;
-  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(out, 16) || !aligned(ws, 16) || !aligned(tree_mask, 8))
+  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(out, 32) || !aligned(ws, 32) || !aligned(tree_mask, 8))
     return IDX_ERR_ALIGN;
   const int64_t rows = static_cast<int64_t>(B) * n;
   if (rows > kMaxRows / H) return IDX_ERR_SHAPE;
@@ -648,7 +656,7 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
   p.whole = pl.whole;
   p.part = static_cast<float*>(ws);
   p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(ws) + pl.part_bytes);
-  p.polls = static_cast<uint32_t>(std::min<unsigned long long>(debug_state().budget_ns / 20, 0xFFFFFF00ull));
+  p.budget_ns = debug_state().budget_ns;
   p.err = device_error_word();
   if (!p.err) return check_launch();
   auto* s = reinterpret_cast<cudaStream_t>(stream);
@@ -657,6 +665,6 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
                 : pl.M == 64 ? launch<64>(tq, p, ctas, s)
                              : launch_tree_mla_wide(tq, p, ctas, s);
   if (r || p.whole) return r;
-  tree_mla_join_kernel<<<dim3(static_cast<unsigned>(ctas), kJoinY), kJoinGroups * 128, 0, s>>>(p);
+  tree_mla_join_kernel<<<dim3(static_cast<unsigned>(ctas), kJoinY), kJoinThreads, 0, s>>>(p);
   return check_launch();
 }

@@ -64,7 +64,7 @@ struct TreeParams {
   int teams, whole;                           // whole: items are not cut
   float* part;                                // [CTA][2] partial slots: M · (512 / halves) outputs, M maxima, M sums
   Cut* cuts;                                  // [CTA]
-  uint32_t polls;                             // bound of every wait
+  unsigned long long budget_ns;               // bound of every wait
   unsigned int* err;
 };
 
@@ -84,8 +84,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
+// 32 bytes of one thread: a whole sector (32-byte aligned)
+__device__ __forceinline__ void st_global32(void* dst, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
@@ -158,34 +162,40 @@ __device__ __forceinline__ bool bar_named_any(int id, int count, bool v) {
       : "memory");
   return r != 0;
 }
-// A warp's wait for a phase of an mbarrier, bounded by a number of polls (at least
-// 20 ns each); false once this CTA has given up.  Short and without the global
-// timer, whose read takes about 1 000 cycles: a wait that succeeds at once costs
-// some 60 cycles instead of 300, and there are a dozen per tile on the critical
-// path.  The vote makes the answer uniform for the compiler, so that what the MMA
-// issue computes stays in uniform registers.  nap: about 50 ns between polls,
-// where nobody waits for this warp, so that the shared-memory queue stays free.
+// A warp's wait for a phase of an mbarrier, for at most budget_ns; false once this
+// CTA has given up.  The global timer, whose read takes about 1 000 cycles, is
+// looked at every 256 polls only: a wait that succeeds at once costs some 60
+// cycles instead of 300, and there are a dozen per tile on the critical path.
+// The vote makes the answer uniform for the compiler, so that what the MMA issue
+// computes stays in uniform registers.  nap: about 50 ns between polls, where
+// nobody waits for this warp, so that the shared-memory queue stays free.
 struct Waits {
-  uint32_t polls;
+  uint64_t budget_ns;
   volatile int* abort_flag;
   unsigned int* err;
   template <bool kNap>
   __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) const {
-    for (uint32_t i = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++i) {
-      if ((i & 63) == 63 && __any_sync(0xFFFFFFFFu, *abort_flag || i > polls)) {
-        if (!*abort_flag) raise_error(err, IDX_DEV_ERR_TIMEOUT);
-        *abort_flag = 1;
-        return false;
-      }
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++i) {
+      if ((i & 255) == 0 && gave_up(t0)) return false;
       if (kNap) __nanosleep(40);
     }
     return true;
+  }
+  __device__ __noinline__ bool gave_up(uint64_t& t0) const {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    const bool late = __any_sync(0xFFFFFFFFu, now - t0 > budget_ns);
+    if (late && !*abort_flag) raise_error(err, IDX_DEV_ERR_TIMEOUT);
+    if (late) *abort_flag = 1;
+    return __any_sync(0xFFFFFFFFu, *abort_flag);
   }
   __device__ __forceinline__ bool nap(uint64_t* bar, uint32_t parity) const { return poll<true>(bar, parity); }
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const { return poll<false>(bar, parity); }
   // during teardown: whatever happened before, wait (the whole warp) for what is in flight
   __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
-    for (uint32_t i = 0; i <= polls && !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++i) {}
+    const uint64_t t0 = globaltimer_ns();
+    while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity) || globaltimer_ns() - t0 > budget_ns)) {}
   }
 };
 
@@ -290,6 +300,11 @@ struct PlanState {
   }
 };
 
+// a / b for a ≥ 0 whose result fits an int (a 64-bit division takes some 500 cycles)
+__device__ __forceinline__ int quotient(long long a, int b) {
+  return a <= 0x7FFFFFFF ? static_cast<int>(a) / b : static_cast<int>(a / b);
+}
+
 struct Share {
   long long size, begin, end;                 // in tiles (in items where they are not cut)
 };
@@ -356,17 +371,19 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
   int b = ms.start_b;
   long long off = ms.start_off;
   Cut cut{0, 0, 0};
-  Seq s{};
+  Seq s{}, ahead{};                           // this sequence, the next one
   if (b < p.B) s = seq_info<M, KT>(p, b, false);
+  if (b + 1 < p.B) ahead = seq_info<M, KT>(p, b + 1, false);
   while (ok && cur < sh.end) {
     const int weight = p.whole ? 1 : s.tiles;
     if (off >= static_cast<long long>(s.items) * weight) {
       if (++b >= p.B) break;
-      s = seq_info<M, KT>(p, b, false);
+      s = ahead;
+      if (b + 1 < p.B) ahead = seq_info<M, KT>(p, b + 1, false);
       off = 0;
       continue;
     }
-    const int item = static_cast<int>(off / weight);
+    const int item = p.whole ? static_cast<int>(off) : quotient(off, weight);
     const int t0 = p.whole ? 0 : static_cast<int>(off - static_cast<long long>(item) * weight);
     const int t1 = p.whole ? s.tiles : static_cast<int>(min(static_cast<long long>(s.tiles), t0 + (sh.end - cur)));
     const int step = p.whole ? 1 : t1 - t0;
@@ -383,14 +400,14 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
     if (slot == 1) {
       cut.row0 = row0;
       cut.rows = rows;
-      cut.pieces = static_cast<int>((s.tiles - t1 + sh.size - 1) / sh.size);
+      cut.pieces = sh.size >= s.tiles ? 1 : (s.tiles - t1 + static_cast<int>(sh.size) - 1) / static_cast<int>(sh.size);
     }
     const int nkeys = p.indices ? p.k : s.ctx;
     const int pb = pieces & 1;
     if (pieces >= 2 && !(ok = waits.nap(&ms.piece_empty[pb], ((pieces >> 1) - 1) & 1))) break;
     uint64_t any = 0;
     for (int c = lane; c < M; c += 32) {
-      const uint64_t m = c < rows ? draft_mask(p, b, p.indices ? tok : static_cast<int>((lo + c) / p.H), s.cnt) : 0;
+      const uint64_t m = c < rows ? draft_mask(p, b, p.indices ? tok : quotient(lo + c, p.H), s.cnt) : 0;
       ms.mask[pb][c] = m;
       any |= m;
     }
@@ -402,12 +419,22 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
       pc.t1 = t1;
       pc.rows = rows;
       pc.slot = slot;
-      pc.mixed = !p.indices && lo / p.H != (lo + rows - 1) / p.H;
+      pc.mixed = !p.indices && quotient(lo, p.H) != quotient(lo + rows - 1, p.H);
       pc.nkeys = nkeys;
       pc.row0 = row0;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms.piece_full[pb]);
+    if (kPrefetch) {
+      // its queries into L2, and what the next item's planning will read first
+      const uint8_t* at = reinterpret_cast<const uint8_t*>(p.q + row0 * kRow);
+      for (int i = rank * 32 + lane; i < rows * 9; i += 32 * p.halves) prefetch_l2(at + static_cast<int64_t>(i) * 128);
+      const int64_t bi = static_cast<int64_t>(b) * p.n + tok;
+      const bool more = tok + 1 < s.cnt;      // the next token, or the next sequence's first
+      if (lane < 2 && lane * 32 < p.k && (more || b + 1 < p.B))
+        prefetch_l2(p.indices + (more ? bi + 1 : static_cast<int64_t>(b + 1) * p.n) * p.k + lane * 32);
+      if (lane == 2 && b + 1 < p.B) prefetch_l2(p.table + static_cast<int64_t>(b + 1) * p.max_pages);
+    }
     // ---- its tiles: lane ↔ keys E·lane …  The positions of tile t + 2 and the
     // page numbers of tile t + 1 are fetched while tile t is published
     const int32_t* sel = p.indices ? p.indices + (static_cast<int64_t>(b) * p.n + tok) * p.k : nullptr;
@@ -459,20 +486,6 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
           pos_far[e] = position(t + 2, e);
         }
       }
-      if (kPrefetch && lane % p.halves == rank) {
-        // into L2, ahead of the copies: each CTA of the team asks for its share of the rows
-        const uint8_t* at = reinterpret_cast<const uint8_t*>(p.cache);
-        bool run = row[0] >= 0;
-#pragma unroll
-        for (int e = 1; e < E; ++e) run &= row[e] == row[0] + e;
-        if (run) {
-          prefetch_l2(at + static_cast<int64_t>(row[0]) * (2 * kRow), E * 2 * kRow);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (row[e] >= 0) prefetch_l2(at + static_cast<int64_t>(row[e]) * (2 * kRow), 2 * kRow);
-        }
-      }
       const int par = tiles % kAhead;
       // free once the copies and the softmax have read what it said kAhead tiles ago
       if (tiles >= kAhead && !(ok = waits.nap(&ms.tile_read[par], (tiles / kAhead - 1) & 1))) break;
@@ -485,6 +498,14 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.tile_full[par]);
       ++tiles;
+      if (kPrefetch) {
+        // the tile's 128-byte lines into L2, ahead of its copies: each CTA of the
+        // team asks for its share
+        for (int i = rank * 32 + lane; i < KT * 9; i += 32 * p.halves) {
+          const int r = ms.row[par][i / 9];
+          if (r >= 0) prefetch_l2(reinterpret_cast<const uint8_t*>(p.cache) + static_cast<int64_t>(r) * (2 * kRow) + i % 9 * 128);
+        }
+      }
       if (t == t0) {                          // its queries, once the last piece's are no longer read
         if (pieces >= 1 && !(ok = waits.nap(&ms.q_empty, (pieces - 1) & 1))) break;
         if (elect_one()) load_q(static_cast<int>(row0));

@@ -56,7 +56,7 @@ static_assert(kColS + kKeys <= kColO, "TMEM columns");
 
 struct WideState : PlanState<kRows, kKeys, kThreads / 32> {
   float top[2][kRows], sum[2][kRows];         // per half of the keys
-  uint64_t v_full[kVs], v_empty[kVs], x_full[2], x_empty[kXs];
+  uint64_t v_full[kVs], v_empty[kVs], x_full[2], x_done;
   uint64_t q_ready, s_full, s_free, p_full, p_free, o_full, o_free, drain_bar;
 };
 constexpr int kSmem = 1024 + kOffMisc + static_cast<int>(sizeof(WideState));
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
   const int half = rank;
-  const Waits waits{p.polls, &ms.abort_flag, p.err};
+  const Waits waits{p.budget_ns, &ms.abort_flag, p.err};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kVs; ++i) {
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ms.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&ms.x_full[i], kCopyWarps * 32);
-    for (int i = 0; i < kXs; ++i) mbar_init(&ms.x_empty[i], 1);
+    mbar_init(&ms.x_done, 1);
     mbar_init(&ms.q_ready, kSoftWarps);
     mbar_init(&ms.s_full, 1);
     mbar_init(&ms.s_free, kSoftWarps);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp == 0) {
-    plan<kRows, kKeys, true>(p, ms, share, rank, waits, [&](int row0) {
+    plan<kRows, kKeys, false>(p, ms, share, rank, waits, [&](int row0) {
       mbar_arrive_expect_tx(&ms.q_full, 3 * kQChunk);
       for (int c = 0; c < 3; ++c)
         tma_box(smem_base + kOffQ + c * kQChunk, &tmap_q, smem_u32(&ms.q_full), feature_chunk(kQTmem + c, half) * 64,
@@ -119,11 +119,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t p_desc = smem_desc_k128_sw128(smem_base + kOffP);
     const uint64_t v_desc = desc_mn(smem_base, kChunk);
     bool ok = true, issued = false;
-    int xs = 0, tiles = 0, pieces = 0;         // running counts (tiles: scores issued)
+    int xs = 0, tiles = 0, pieces = 0;         // next x buffer; running counts (tiles: scores issued)
     while (true) {
       const int pb = pieces & 1;
       if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
-      const int n = __shfl_sync(0xFFFFFFFFu, ms.piece[pb].t1 - ms.piece[pb].t0, 0);
+      const int n = __reduce_max_sync(0xFFFFFFFFu, ms.piece[pb].t1 - ms.piece[pb].t0);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
       if (n == 0) break;
@@ -131,39 +131,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c <= n && ok; ++c) {
         if (c < n) {
           // S = q · Kᵀ of tile c, once the softmax has read the last S
-          if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
+          const int sl = tiles % kVs;
           if (!(ok = waits(&ms.x_full[tiles & 1], (tiles >> 1) & 1))) break;
+          if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
           fence_proxy_async_smem();            // the copies wrote through the generic proxy
+          if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
           tc_fence_after();
           if (elect_one()) {
-#pragma unroll
+            int x = xs;
+#pragma unroll 1
             for (int u = 0; u < 5; ++u) {
-              const int sl = (xs + u) % kXs;
-              const uint64_t b = k_desc + static_cast<uint64_t>((kOffX + sl * kChunk) >> 4);
+              const uint64_t b = k_desc + static_cast<uint64_t>((kOffX >> 4) + x * (kChunk >> 4));
 #pragma unroll
               for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + u * 32 + i * 8, b + i * 2, id_s, (u > 0 || i > 0) ? 1u : 0u);
-              mma_commit(&ms.x_empty[sl]);
+              x = x == kXs - 1 ? 0 : x + 1;
             }
-          }
-          issued = true;
-          __syncwarp();
-          xs += 5;
-          const int sl = tiles % kVs;
-          if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
-          fence_proxy_async_smem();
-          tc_fence_after();
-          if (elect_one()) {
+            mma_commit(&ms.x_done);
             const uint64_t b = k_desc + static_cast<uint64_t>(sl * (kV >> 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + 5 * 32 + i * 8, b + i * 2, id_s, 1u);
+#pragma unroll 1
+            for (int u = 0; u < 3; ++u)
 #pragma unroll
-            for (int i = 0; i < 12; ++i)
-              mma_f16(d_s, q_desc + static_cast<uint64_t>((i >> 2) * (kQChunk >> 4) + (i & 3) * 2),
-                      b + static_cast<uint64_t>(((i >> 2) + 1) * (kChunk >> 4) + (i & 3) * 2), id_s, 1u);
+              for (int i = 0; i < 4; ++i)
+                mma_f16(d_s, q_desc + static_cast<uint64_t>(u * (kQChunk >> 4) + i * 2),
+                        b + static_cast<uint64_t>((u + 1) * (kChunk >> 4) + i * 2), id_s, 1u);
             mma_commit(&ms.s_full);
             if (c == n - 1) mma_commit(&ms.q_empty);
           }
+          issued = true;
           __syncwarp();
+          xs = (xs + 5) % kXs;
           ++tiles;
         }
         if (c >= 1) {
@@ -217,15 +215,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 2; ++j) xrow[j] = ms.row[par][key1 + 32 * j];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.tile_read[par]);
+      // chunk 5·t + u takes the place of the one seven earlier: of tile t − 2 for
+      // the first two (waited for at tile t − 1), of tile t − 1 for the others
+#pragma unroll
       for (int u = 0; u < 5; ++u) {
-        const int sl = xs % kXs;
-        if (xs >= kXs && !(ok = waits.nap(&ms.x_empty[sl], (xs / kXs - 1) & 1))) break;
+        if (u == 2 && tiles >= 1 && !(ok = waits.nap(&ms.x_done, (tiles - 1) & 1))) break;
         const uint8_t* src = from + feature_chunk(u, half) * 128 + (lane & 7) * 16;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          cp_async16(to_x + sl * kChunk + j * 4096, src + static_cast<int64_t>(max(xrow[j], 0)) * (2 * kRow),
+          cp_async16(to_x + xs * kChunk + j * 4096, src + static_cast<int64_t>(max(xrow[j], 0)) * (2 * kRow),
                      xrow[j] >= 0 ? 16 : 0);
-        ++xs;
+        xs = xs == kXs - 1 ? 0 : xs + 1;
       }
       if (!ok) break;
       cp_async_arrive(&ms.x_full[tiles & 1]);
@@ -419,22 +419,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld<16>(lanes + kColO + part * (kHalf / 2) + q, o);
         tmem_wait();
         regs_ready<16>(o);
-        float x[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(o[c]) * inv;
-        if (!whole || !p.out_bf16) {
+        if (!have) {
+          // (the loads are for all lanes)
+        } else if (!whole || !p.out_bf16) {
           float* dst = whole ? static_cast<float*>(p.out) + at + q : slot + r_id * kHalf + part * (kHalf / 2) + q;
-          if (have) {
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
-          }
-        } else if (have) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + q);
+          for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+          st_global32(dst, o);
+          st_global32(dst + 8, o + 8);
+        } else {
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            dst[c] = make_uint4(bf_pack(x[8 * c], x[8 * c + 1]), bf_pack(x[8 * c + 2], x[8 * c + 3]),
-                                bf_pack(x[8 * c + 4], x[8 * c + 5]), bf_pack(x[8 * c + 6], x[8 * c + 7]));
+          for (int c = 0; c < 8; ++c)
+            o[c] = bf_pack(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
+          st_global32(static_cast<__nv_bfloat16*>(p.out) + at + q, o);
         }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
