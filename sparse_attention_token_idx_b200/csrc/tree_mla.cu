@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp == 0) {
-    plan<N, kTile, false>(p, ms, share, rank, waits, [&](int row0) {
+    plan<N, kTile>(p, ms, share, rank, waits, [&](int row0) {
       mbar_arrive_expect_tx(&ms.q_full, 9 * N * 128);
       for (int c = 0; c < 9; ++c)
         tma_box(smem_base + C::kOffQ + c * N * 128, &tmap_q, smem_u32(&ms.q_full), c * 64, row0);

@@ -190,6 +190,17 @@ struct Waits {
     if (late) *abort_flag = 1;
     return __any_sync(0xFFFFFFFFu, *abort_flag);
   }
+  __device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) const {
+    uint32_t ok;                              // (try_wait would suspend the thread for a while)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xFFFFFFFFu, ok != 0);
+  }
   __device__ __forceinline__ bool nap(uint64_t* bar, uint32_t parity) const { return poll<true>(bar, parity); }
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const { return poll<false>(bar, parity); }
   // during teardown: whatever happened before, wait (the whole warp) for what is in flight
@@ -360,7 +371,7 @@ __device__ __forceinline__ Share find_share(const TreeParams& p, State& ms, int 
 // The planner warp: walks the share, publishes each piece (tile range, what its
 // rows see of the drafts) and each tile (cache rows of its keys), and has the
 // piece's queries loaded: load_q(row0) issues them on ms.q_full.
-template <int M, int KT, bool kPrefetch, class State, class LoadQ>
+template <int M, int KT, class State, class LoadQ>
 __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share& sh, int rank, const Waits& waits,
                                      LoadQ load_q) {
   constexpr int E = KT / 32;                  // keys per lane
@@ -425,16 +436,6 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms.piece_full[pb]);
-    if (kPrefetch) {
-      // its queries into L2, and what the next item's planning will read first
-      const uint8_t* at = reinterpret_cast<const uint8_t*>(p.q + row0 * kRow);
-      for (int i = rank * 32 + lane; i < rows * 9; i += 32 * p.halves) prefetch_l2(at + static_cast<int64_t>(i) * 128);
-      const int64_t bi = static_cast<int64_t>(b) * p.n + tok;
-      const bool more = tok + 1 < s.cnt;      // the next token, or the next sequence's first
-      if (lane < 2 && lane * 32 < p.k && (more || b + 1 < p.B))
-        prefetch_l2(p.indices + (more ? bi + 1 : static_cast<int64_t>(b + 1) * p.n) * p.k + lane * 32);
-      if (lane == 2 && b + 1 < p.B) prefetch_l2(p.table + static_cast<int64_t>(b + 1) * p.max_pages);
-    }
     // ---- its tiles: lane ↔ keys E·lane …  The positions of tile t + 2 and the
     // page numbers of tile t + 1 are fetched while tile t is published
     const int32_t* sel = p.indices ? p.indices + (static_cast<int64_t>(b) * p.n + tok) * p.k : nullptr;
@@ -498,14 +499,6 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.tile_full[par]);
       ++tiles;
-      if (kPrefetch) {
-        // the tile's 128-byte lines into L2, ahead of its copies: each CTA of the
-        // team asks for its share
-        for (int i = rank * 32 + lane; i < KT * 9; i += 32 * p.halves) {
-          const int r = ms.row[par][i / 9];
-          if (r >= 0) prefetch_l2(reinterpret_cast<const uint8_t*>(p.cache) + static_cast<int64_t>(r) * (2 * kRow) + i % 9 * 128);
-        }
-      }
       if (t == t0) {                          // its queries, once the last piece's are no longer read
         if (pieces >= 1 && !(ok = waits.nap(&ms.q_empty, (pieces - 1) & 1))) break;
         if (elect_one()) load_q(static_cast<int>(row0));

@@ -13,20 +13,23 @@
 // The tile's nine 64-feature chunks live in two rings: the four that are also
 // this CTA's V (three buffers: free after the product) and the five others (a ring
 // of seven: free after the scores).  So the copies of the next tile wait neither
-// for this tile's softmax nor for its product, and the MMA warp issues the scores of
-// tile t + 1 before the product of tile t: the softmax of t runs under them.
+// for this tile's softmax nor for its product, and the scores of tile t + 1 run while
+// the softmax of t does.  Scores and products are issued by two warps: what a warp asks of
+// a barrier waits behind the MMAs that it has queued (some 400 cycles of them).
 //
-// One CTA, 18 warps:
+// One CTA, 20 warps:
 //   warp 0       the planner (tree_mla.cuh);
-//   warp 1       issues the MMAs;
-//   warps 2-9    copy the rows by cp.async, 16 bytes a lane (a key that no row sees
+//   warps 1, 2   issue the MMAs of the scores and of the products;
+//   warps 3-10   copy the rows by cp.async, 16 bytes a lane (a key that no row sees
 //                arrives as zeros);
-//   warps 10-17  softmax: thread ↔ (row, half of the keys), the row's reference
+//   warps 11-18  softmax: thread ↔ (row, half of the keys), the row's reference
 //                maximum in a register, raised only where a score passes it by 2^8
 //                (then the two threads of a row agree through shared memory and O
 //                in TMEM is rescaled); P = 2^(s − m) in bf16 in shared memory;
 //                between pieces they put the next queries' first six chunks into
-//                TMEM while the last product runs.
+//                TMEM while the last product runs;
+//   warp 19      asks for the tiles' lines in L2 a few tiles ahead of the copies (the
+//                rings hold a tile and a half, less than the latency of HBM).
 // Rounding, bounded waits and the way out as in tree_mla.cu.
 #include "tree_mla.cuh"
 
@@ -39,8 +42,9 @@ constexpr int kRows = 128;                    // rows per CTA
 constexpr int kKeys = 64;                     // keys per tile
 constexpr int kHalf = 256;                    // output features per CTA
 constexpr int kCopyWarps = 8, kSoftWarps = 8;
-constexpr int kFirstSoft = 2 + kCopyWarps;
-constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
+constexpr int kFirstCopy = 3, kFirstSoft = kFirstCopy + kCopyWarps;
+constexpr int kPrefetchWarp = kFirstSoft + kSoftWarps;
+constexpr int kThreads = (kPrefetchWarp + 1) * 32;
 constexpr int kChunk = kKeys * 128;           // 64 keys × 64 features
 constexpr int kV = 4 * kChunk;                // a V buffer
 constexpr int kVs = 3, kXs = 7;               // buffers of V, and of the other chunks
@@ -57,7 +61,7 @@ static_assert(kColS + kKeys <= kColO, "TMEM columns");
 struct WideState : PlanState<kRows, kKeys, kThreads / 32> {
   float top[2][kRows], sum[2][kRows];         // per half of the keys
   uint64_t v_full[kVs], v_empty[kVs], x_full[2], x_done;
-  uint64_t q_ready, s_full, s_free, p_full, p_free, o_full, o_free, drain_bar;
+  uint64_t q_ready, s_full, s_free, p_full, p_free, o_full, o_free, drain_bar[2];
 };
 constexpr int kSmem = 1024 + kOffMisc + static_cast<int>(sizeof(WideState));
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -92,8 +96,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ms.p_free, 1);
     mbar_init(&ms.o_full, 1);
     mbar_init(&ms.o_free, kSoftWarps);
-    mbar_init(&ms.drain_bar, 1);
-    ms.init(p.B, kCopyWarps + kSoftWarps, kSoftWarps + 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ms.drain_bar[i], 1);
+    ms.init(p.B, kCopyWarps + kSoftWarps + 1, kSoftWarps + 2);
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
   }
@@ -103,23 +107,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp == 0) {
-    plan<kRows, kKeys, false>(p, ms, share, rank, waits, [&](int row0) {
+    plan<kRows, kKeys>(p, ms, share, rank, waits, [&](int row0) {
       mbar_arrive_expect_tx(&ms.q_full, 3 * kQChunk);
       for (int c = 0; c < 3; ++c)
         tma_box(smem_base + kOffQ + c * kQChunk, &tmap_q, smem_u32(&ms.q_full), feature_chunk(kQTmem + c, half) * 64,
                 row0);
     });
   } else if (warp == 1) {
-    // ================================================================ MMA issuer
+    // ================================================================ scores
     const uint32_t id_s = idesc_bf16(kKeys, false, false) | (p.scale_log2 < 0.f ? kNegateA : 0u);
-    constexpr uint32_t id_o = idesc_bf16(kHalf, false, true);
-    const uint32_t d_s = tmem + kColS, d_o = tmem + kColO;
+    const uint32_t d_s = tmem + kColS;
     const uint64_t k_desc = smem_desc_k128_sw128(smem_base);
     const uint64_t q_desc = smem_desc_k128_sw128(smem_base + kOffQ);
-    const uint64_t p_desc = smem_desc_k128_sw128(smem_base + kOffP);
-    const uint64_t v_desc = desc_mn(smem_base, kChunk);
     bool ok = true, issued = false;
-    int xs = 0, tiles = 0, pieces = 0;         // next x buffer; running counts (tiles: scores issued)
+    int xs = 0, tiles = 0, pieces = 0;         // next x buffer; running counts
     while (true) {
       const int pb = pieces & 1;
       if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
@@ -128,69 +129,92 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
       if (n == 0) break;
       if (!(ok = waits(&ms.q_full, pieces & 1)) || !(ok = waits(&ms.q_ready, pieces & 1))) break;
-      for (int c = 0; c <= n && ok; ++c) {
-        if (c < n) {
-          // S = q · Kᵀ of tile c, once the softmax has read the last S
-          const int sl = tiles % kVs;
-          if (!(ok = waits(&ms.x_full[tiles & 1], (tiles >> 1) & 1))) break;
-          if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
-          fence_proxy_async_smem();            // the copies wrote through the generic proxy
-          if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            int x = xs;
+      for (int c = 0; c < n; ++c) {
+        // S = q · Kᵀ of tile c, once the softmax has read the last S
+        const int sl = tiles % kVs;
+        if (!(ok = waits(&ms.x_full[tiles & 1], (tiles >> 1) & 1))) break;
+        if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
+        fence_proxy_async_smem();              // the copies wrote through the generic proxy
+        if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          int x = xs;
 #pragma unroll 1
-            for (int u = 0; u < 5; ++u) {
-              const uint64_t b = k_desc + static_cast<uint64_t>((kOffX >> 4) + x * (kChunk >> 4));
+          for (int u = 0; u < 5; ++u) {
+            const uint64_t b = k_desc + static_cast<uint64_t>((kOffX >> 4) + x * (kChunk >> 4));
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + u * 32 + i * 8, b + i * 2, id_s, (u > 0 || i > 0) ? 1u : 0u);
-              x = x == kXs - 1 ? 0 : x + 1;
-            }
-            mma_commit(&ms.x_done);
-            const uint64_t b = k_desc + static_cast<uint64_t>(sl * (kV >> 4));
+            for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + u * 32 + i * 8, b + i * 2, id_s, (u > 0 || i > 0) ? 1u : 0u);
+            x = x == kXs - 1 ? 0 : x + 1;
+          }
+          mma_commit(&ms.x_done);
+          const uint64_t b = k_desc + static_cast<uint64_t>(sl * (kV >> 4));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + 5 * 32 + i * 8, b + i * 2, id_s, 1u);
+          for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + 5 * 32 + i * 8, b + i * 2, id_s, 1u);
 #pragma unroll 1
-            for (int u = 0; u < 3; ++u)
+          for (int u = 0; u < 3; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_f16(d_s, q_desc + static_cast<uint64_t>(u * (kQChunk >> 4) + i * 2),
-                        b + static_cast<uint64_t>((u + 1) * (kChunk >> 4) + i * 2), id_s, 1u);
-            mma_commit(&ms.s_full);
-            if (c == n - 1) mma_commit(&ms.q_empty);
-          }
-          issued = true;
-          __syncwarp();
-          xs = (xs + 5) % kXs;
-          ++tiles;
+            for (int i = 0; i < 4; ++i)
+              mma_f16(d_s, q_desc + static_cast<uint64_t>(u * (kQChunk >> 4) + i * 2),
+                      b + static_cast<uint64_t>((u + 1) * (kChunk >> 4) + i * 2), id_s, 1u);
+          mma_commit(&ms.s_full);
+          if (c == n - 1) mma_commit(&ms.q_empty);
         }
-        if (c >= 1) {
-          // O += P · V of tile c − 1
-          const int t = tiles - (c < n ? 2 : 1);
-          if (!(ok = waits(&ms.p_full, t & 1))) break;
-          if (c == 1 && pieces > 0 && !(ok = waits(&ms.o_free, (pieces - 1) & 1))) break;
-          fence_proxy_async_smem();
-          tc_fence_after();
-          if (elect_one()) {
-            const int sl = t % kVs;
-            const uint64_t b = v_desc + static_cast<uint64_t>(sl * (kV >> 4));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)         // 16 keys per instruction: two 8-row atoms
-              mma_f16(d_o, p_desc + i * 2, b + i * (2048 >> 4), id_o, (c > 1 || i > 0) ? 1u : 0u);
-            mma_commit(&ms.p_free);
-            mma_commit(&ms.v_empty[sl]);
-            if (c == n) mma_commit(&ms.o_full);
-          }
-          __syncwarp();
-        }
+        issued = true;
+        __syncwarp();
+        xs = (xs + 5) % kXs;
+        ++tiles;
       }
       if (!ok) break;
       ++pieces;
     }
     if (issued) {
-      if (elect_one()) mma_commit(&ms.drain_bar);
+      if (elect_one()) mma_commit(&ms.drain_bar[0]);
       __syncwarp();
-      waits.drain(&ms.drain_bar, 0);
+      waits.drain(&ms.drain_bar[0], 0);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ================================================================ products
+    constexpr uint32_t id_o = idesc_bf16(kHalf, false, true);
+    const uint32_t d_o = tmem + kColO;
+    const uint64_t p_desc = smem_desc_k128_sw128(smem_base + kOffP);
+    const uint64_t v_desc = desc_mn(smem_base, kChunk);
+    bool ok = true, issued = false;
+    int tiles = 0, pieces = 0;
+    while (true) {
+      const int pb = pieces & 1;
+      if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
+      const int n = __reduce_max_sync(0xFFFFFFFFu, ms.piece[pb].t1 - ms.piece[pb].t0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
+      if (n == 0) break;
+      for (int c = 0; c < n; ++c) {
+        // O += P · V of tile c (its scores, and so its V, were complete before its P)
+        const int sl = tiles % kVs;
+        if (c == 0 && pieces > 0 && !(ok = waits(&ms.o_free, (pieces - 1) & 1))) break;
+        if (!(ok = waits(&ms.p_full, tiles & 1))) break;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t b = v_desc + static_cast<uint64_t>(sl * (kV >> 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)           // 16 keys per instruction: two 8-row atoms
+            mma_f16(d_o, p_desc + i * 2, b + i * (2048 >> 4), id_o, (c > 0 || i > 0) ? 1u : 0u);
+          mma_commit(&ms.p_free);
+          mma_commit(&ms.v_empty[sl]);
+          if (c == n - 1) mma_commit(&ms.o_full);
+        }
+        issued = true;
+        __syncwarp();
+        ++tiles;
+      }
+      if (!ok) break;
+      ++pieces;
+    }
+    if (issued) {
+      if (elect_one()) mma_commit(&ms.drain_bar[1]);
+      __syncwarp();
+      waits.drain(&ms.drain_bar[1], 0);
     }
     __syncwarp();
   } else if (warp < kFirstSoft) {
@@ -198,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // V: a warp instruction copies 512 bytes of key w + 8·j.  The other chunks:
     // 128 bytes of the four keys 4·w + 32·j ….  Piece c of row r goes to
     // (c mod 8) ^ (r mod 8) of its 128-byte row, as the descriptors say.
-    const int w = warp - 2;
+    const int w = warp - kFirstCopy;
     const uint32_t to_v = smem_base + (lane >> 3) * kChunk + w * 128 + (((lane & 7) ^ (w & 7)) << 4);
     const int key1 = 4 * w + (lane >> 3);
     const uint32_t to_x = smem_base + kOffX + key1 * 128 + (((lane & 7) ^ (key1 & 7)) << 4);
@@ -239,6 +263,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++tiles;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");       // they have landed before the memory goes
+  } else if (warp == kPrefetchWarp) {
+    // ================================================================ prefetch
+    // the tiles' 128-byte lines into L2, up to kAhead tiles before their copies:
+    // each CTA of the team asks for its half
+    for (int tiles = 0;; ++tiles) {
+      const int par = tiles % kAhead;
+      if (!waits.nap(&ms.tile_full[par], (tiles / kAhead) & 1) || ms.last[par]) break;
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
+#pragma unroll
+      for (int i = 0; i < kKeys * 9 / 64; ++i) {
+        const int line = i * 64 + half * 32 + lane, r = ms.row[par][line / 9];
+        if (r >= 0) prefetch_l2(from + static_cast<int64_t>(r) * (2 * kRow) + line % 9 * 128);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.tile_read[par]);
+    }
   } else {
     // ================================================================ softmax
     const int sw = warp - kFirstSoft, quad = warp & 3, part = sw >> 2;
@@ -292,6 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int sh = pc.nkeys - (t * kKeys + part * 32);   // key of draft 0 in these 32
           const uint64_t at = sh >= 0 ? (sh < 64 ? drafts << sh : 0) : (sh > -64 ? drafts >> -sh : 0);
           sees |= static_cast<uint32_t>(at) & dr;
+        }
+        if (t == pc.t1 - 1 && waits.test(&ms.piece_full[pb ^ 1], ((pieces + 1) >> 1) & 1)) {
+          const Piece& next = ms.piece[pb ^ 1];            // its queries into L2 (load_q reads them soon)
+          if (next.t0 != next.t1 && r_id < next.rows)
+            for (int i = 0; i < 3; ++i)
+              prefetch_l2(p.q + (next.row0 + r_id) * kRow + feature_chunk(part * 3 + i, half) * 64);
         }
         if (!(ok = waits(&ms.s_full, tiles & 1))) break;
         tc_fence_after();
