@@ -17,15 +17,17 @@
 // delivers to one SM in about 6 500: small N is bound by HBM, N = 64 by the MMAs
 // and the shared-memory bandwidth that they take.
 //
-// One CTA, 16 warps (24 for N = 64):
+// One CTA, 15 warps (23 for N = 64):
 //   warp 0     the planner (tree_mla.cuh);
-//   warp 1     issues the MMAs: scores of tile t, then its product, so that tile
-//              t + 1 streams into the parts of the buffer that the product has freed;
-//   warps 2-7  copy the tiles' rows by cp.async, 16 bytes a lane; a key that no row
+//   warps 1, 2 issue the MMAs of the scores and of the products (two warps, since what
+//              one asks of a barrier waits behind the MMAs that it has queued): the
+//              product of tile t frees the latent buffers one by one, and tile t + 1
+//              streams into them and through the scores;
+//   warps 3-6  copy the tiles' rows by cp.async, 16 bytes a lane; a key that no row
 //              sees arrives as zeros, never as what memory holds.  (TMA delivers these
 //              1 152-byte rows at 25 B/clk per SM in boxes and 9 – 20 gathered, cp.async
 //              at 34 – 70 with 4 – 16 warps from L2 and 26 from HBM, its limit.)
-//   warps 8 …  softmax: thread ↔ (key, part of the rows).  Scores are compared with
+//   warps 7 …  softmax: thread ↔ (key, part of the rows).  Scores are compared with
 //              a running reference maximum per row as it is; only where one passes it
 //              by 2^8 (a piece's first tile always) the column maxima are reduced, by a
 //              transposing butterfly across lanes and shared memory across warps, the
@@ -44,8 +46,9 @@ using namespace tree;
 constexpr int kTile = 128;                    // keys per tile
 constexpr int kPair = 32768;                  // 128 keys × 128 latent features: two 64-feature chunks
 constexpr int kChunk = 16384;                 // 128 keys × 64 features
-constexpr int kCopyWarps = 6;                 // warps that copy the tiles
-constexpr int kFirstSoft = 2 + kCopyWarps;    // planner, MMA issuer, copies, then the softmax
+constexpr int kCopyWarps = 4;                 // warps that copy the tiles
+constexpr int kFirstCopy = 3;                 // planner, the two MMA issuers, copies, then the softmax
+constexpr int kFirstSoft = kFirstCopy + kCopyWarps;
 
 template <int N>
 struct Cfg {
@@ -70,7 +73,7 @@ struct Misc : PlanState<N, kTile, Cfg<N>::kThreads / 32> {
   alignas(16) float alpha[Cfg<N>::kSoftWarps][Cfg<N>::kNC];
   alignas(16) float sum[Cfg<N>::kParts][4][Cfg<N>::kNC];
   uint64_t pair_full[5], pair_empty[5], rope_full[2], rope_empty[2];
-  uint64_t s_full, p_full, o_full, o_free, drain_bar;
+  uint64_t s_full, s_free, p_full, p_free, o_full, o_free, drain_bar[2];
 };
 
 // Column reduction of v[NC] over the warp's 32 lanes by a transposing butterfly;
@@ -119,11 +122,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       mbar_init(&ms.rope_empty[i], 1);
     }
     mbar_init(&ms.s_full, 1);
+    mbar_init(&ms.s_free, C::kSoftWarps);
     mbar_init(&ms.p_full, C::kSoftWarps);
+    mbar_init(&ms.p_free, 1);
     mbar_init(&ms.o_full, 1);
     mbar_init(&ms.o_free, C::kSoftWarps);
-    mbar_init(&ms.drain_bar, 1);
-    ms.init(p.B, kCopyWarps + C::kSoftWarps, C::kSoftWarps + 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ms.drain_bar[i], 1);
+    ms.init(p.B, kCopyWarps + C::kSoftWarps, C::kSoftWarps + 2);
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
   }
@@ -139,35 +144,31 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         tma_box(smem_base + C::kOffQ + c * N * 128, &tmap_q, smem_u32(&ms.q_full), c * 64, row0);
     });
   } else if (warp == 1) {
-    // ================================================================ MMA issuer
-    constexpr uint32_t id_o = idesc_bf16(N, true, true);
+    // ================================================================ scores
     // a negative scale turns the scores' signs here, so that the softmax sees a positive one
     const uint32_t id_s = idesc_bf16(N, false, false) | (p.scale_log2 < 0.f ? kNegateA : 0u);
     const uint32_t d_s = tmem + 4 * N;
     const uint64_t q_desc = smem_desc_k128_sw128(smem_base + C::kOffQ);
     const uint64_t k_desc = smem_desc_k128_sw128(smem_base);
-    const uint64_t v_desc = desc_mn(smem_base, kChunk);
-    const uint64_t p_desc = desc_mn(smem_base + C::kOffP, kChunk);
     bool ok = true, issued = false;
-    int pairs = 0, ropes = 0, tiles = 0, pieces = 0;
+    int slot = 0, lap = 0, tiles = 0, pieces = 0;          // latent buffer, times around; running counts
     while (true) {
       const int pb = pieces & 1;
       if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
-      const int t0 = __reduce_max_sync(0xFFFFFFFFu, ms.piece[pb].t0), t1 = __reduce_max_sync(0xFFFFFFFFu, ms.piece[pb].t1);
+      const int n = __reduce_max_sync(0xFFFFFFFFu, ms.piece[pb].t1 - ms.piece[pb].t0);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
-      if (t0 == t1) break;
+      if (n == 0) break;
       if (!(ok = waits(&ms.q_full, pieces & 1))) break;
-      for (int t = t0; t < t1 && ok; ++t) {
-        // Sᵀ = K · qᵀ
-        const int first = pairs;
-        for (int u = 0; u < 4 && ok; ++u) {
-          const int sl = (first + u) % C::kPairs;
-          if (!(ok = waits(&ms.pair_full[sl], ((first + u) / C::kPairs) & 1))) break;
+      for (int c = 0; c < n && ok; ++c) {
+        // Sᵀ = K · qᵀ, once the softmax has read the last S, chunk by chunk as they land
+        if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
+        for (int u = 0; u < 4; ++u) {
+          if (!(ok = waits(&ms.pair_full[slot], lap & 1))) break;
           fence_proxy_async_smem();                        // the copies wrote through the generic proxy
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t a = k_desc + static_cast<uint64_t>(sl * (kPair >> 4));
+            const uint64_t a = k_desc + static_cast<uint64_t>(slot * (kPair >> 4));
             const uint64_t q = q_desc + static_cast<uint64_t>(u * (2 * N * 128 >> 4));
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -176,10 +177,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
           }
           issued = true;
           __syncwarp();
+          if (++slot == C::kPairs) slot = 0, ++lap;
         }
         if (!ok) break;
-        const int rs = ropes % C::kRopes;
-        if (!(ok = waits(&ms.rope_full[rs], (ropes / C::kRopes) & 1))) break;
+        const int rs = tiles % C::kRopes;
+        if (!(ok = waits(&ms.rope_full[rs], (tiles / C::kRopes) & 1))) break;
         fence_proxy_async_smem();
         tc_fence_after();
         if (elect_one()) {
@@ -189,53 +191,83 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
           for (int i = 0; i < 4; ++i) mma_f16(d_s, a + i * 2, q + i * 2, id_s, 1u);
           mma_commit(&ms.s_full);
           if (!C::kAliasP) mma_commit(&ms.rope_empty[rs]);
-          if (t == t1 - 1) mma_commit(&ms.q_empty);
+          if (c == n - 1) mma_commit(&ms.q_empty);
         }
         __syncwarp();
-        // Oᵀ += Vᵀ · Pᵀ
-        if (!(ok = waits(&ms.p_full, tiles & 1))) break;
-        if (t == t0 && pieces > 0 && !(ok = waits(&ms.o_free, (pieces - 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t acc = t > t0 ? 1u : 0u;
-          for (int u = 0; u < 4; ++u) {
-            const int sl = (first + u) % C::kPairs;
-            const uint64_t a = v_desc + static_cast<uint64_t>(sl * (kPair >> 4));
-#pragma unroll
-            for (int i = 0; i < 8; ++i)                    // 16 keys per instruction: two 8-row atoms
-              mma_f16(tmem + u * N, a + i * (2048 >> 4), p_desc + i * (2048 >> 4), id_o, i > 0 ? 1u : acc);
-            mma_commit(&ms.pair_empty[sl]);
-          }
-          if (C::kAliasP) mma_commit(&ms.rope_empty[rs]);
-          if (t == t1 - 1) mma_commit(&ms.o_full);
-        }
-        __syncwarp();
-        pairs += 4;
-        ++ropes;
         ++tiles;
       }
       if (!ok) break;
       ++pieces;
     }
     if (issued) {
-      if (elect_one()) mma_commit(&ms.drain_bar);
+      if (elect_one()) mma_commit(&ms.drain_bar[0]);
       __syncwarp();
-      waits.drain(&ms.drain_bar, 0);
+      waits.drain(&ms.drain_bar[0], 0);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ================================================================ products
+    constexpr uint32_t id_o = idesc_bf16(N, true, true);
+    const uint64_t v_desc = desc_mn(smem_base, kChunk);
+    const uint64_t p_desc = desc_mn(smem_base + C::kOffP, kChunk);
+    bool ok = true, issued = false;
+    int slot = 0, tiles = 0, pieces = 0;
+    while (true) {
+      const int pb = pieces & 1;
+      if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
+      const int n = __reduce_max_sync(0xFFFFFFFFu, ms.piece[pb].t1 - ms.piece[pb].t0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
+      if (n == 0) break;
+      for (int c = 0; c < n; ++c) {
+        // Oᵀ += Vᵀ · Pᵀ (the tile's scores, and so its V, were complete before its P)
+        if (c == 0 && pieces > 0 && !(ok = waits(&ms.o_free, (pieces - 1) & 1))) break;
+        if (!(ok = waits(&ms.p_full, tiles & 1))) break;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        if (elect_one()) {
+          int sl = slot;
+#pragma unroll 1
+          for (int u = 0; u < 4; ++u) {
+            const uint64_t a = v_desc + static_cast<uint64_t>(sl * (kPair >> 4));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)                    // 16 keys per instruction: two 8-row atoms
+              mma_f16(tmem + u * N, a + i * (2048 >> 4), p_desc + i * (2048 >> 4), id_o, (c > 0 || i > 0) ? 1u : 0u);
+            mma_commit(&ms.pair_empty[sl]);
+            if (++sl == C::kPairs) sl = 0;
+          }
+          mma_commit(&ms.p_free);
+          if (C::kAliasP) mma_commit(&ms.rope_empty[tiles % C::kRopes]);
+          if (c == n - 1) mma_commit(&ms.o_full);
+        }
+        issued = true;
+        __syncwarp();
+        slot = (slot + 4) % C::kPairs;
+        ++tiles;
+      }
+      if (!ok) break;
+      ++pieces;
+    }
+    if (issued) {
+      if (elect_one()) mma_commit(&ms.drain_bar[1]);
+      __syncwarp();
+      waits.drain(&ms.drain_bar[1], 0);
     }
     __syncwarp();
   } else if (warp < kFirstSoft) {
     // ================================================================ copies
-    // A warp instruction copies 256 bytes of two rows: lanes 0-15 key 2·w + 12·j,
+    // A warp instruction copies 256 bytes of two rows: lanes 0-15 key 2·w + 8·j,
     // lanes 16-31 the next; piece c of row r goes to (c mod 8) ^ (r mod 8) of its
-    // 128-byte row, the swizzle that the descriptors name (12 rows on, r mod 8 has
-    // its bit 2 turned).  The rotary chunk: 128 bytes of four rows, 24 rows a step.
+    // 128-byte row, the swizzle that the descriptors name.  The rotary chunk: 128
+    // bytes of four rows, 16 rows a step.
     constexpr int kStep = 2 * kCopyWarps, kRopeStep = 4 * kCopyWarps;
-    constexpr int kRuns = (kTile + kStep - 1) / kStep, kRopeRuns = (kTile + kRopeStep - 1) / kRopeStep;
-    static_assert(kStep % 8 == 4 && kRopeStep % 8 == 0, "the swizzle of later runs");
-    const int key0 = 2 * (warp - 2) + (lane >> 4);
+    constexpr int kRuns = kTile / kStep, kRopeRuns = kTile / kRopeStep;
+    static_assert(kStep % 8 == 0 && kTile % kRopeStep == 0, "the swizzle of later runs");
+    const int w = warp - kFirstCopy;
+    const int key0 = 2 * w + (lane >> 4);
     const int piece = lane & 15;
     const uint32_t to_pair = smem_base + (piece >> 3) * kChunk + key0 * 128 + (((piece & 7) ^ (key0 & 7)) << 4);
-    const int key1 = 4 * (warp - 2) + (lane >> 3);
+    const int key1 = 4 * w + (lane >> 3);
     const uint32_t to_rope = smem_base + C::kOffRope + key1 * 128 + (((lane & 7) ^ (key1 & 7)) << 4);
     const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
     int pairs = 0, ropes = 0, tiles = 0;
@@ -243,11 +275,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     while (ok) {
       const int par = tiles % kAhead;
       if (!waits.nap(&ms.tile_full[par], (tiles / kAhead) & 1) || ms.last[par]) break;
-      int row[kRuns], rope_row[kRopeRuns];                 // the last run of some warps is past the tile
+      int row[kRuns], rope_row[kRopeRuns];
 #pragma unroll
-      for (int j = 0; j < kRuns; ++j) row[j] = ms.row[par][min(key0 + kStep * j, kTile - 1)];
+      for (int j = 0; j < kRuns; ++j) row[j] = ms.row[par][key0 + kStep * j];
 #pragma unroll
-      for (int j = 0; j < kRopeRuns; ++j) rope_row[j] = ms.row[par][min(key1 + kRopeStep * j, kTile - 1)];
+      for (int j = 0; j < kRopeRuns; ++j) rope_row[j] = ms.row[par][key1 + kRopeStep * j];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.tile_read[par]);
       for (int u = 0; u < 4; ++u) {
@@ -255,12 +287,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         if (pairs >= C::kPairs && !(ok = waits.nap(&ms.pair_empty[sl], (pairs / C::kPairs - 1) & 1))) break;
         const uint32_t to = to_pair + sl * kPair;
         const uint8_t* src = from + u * 256 + piece * 16;
-        const uint32_t to_odd = to ^ 64;
 #pragma unroll
         for (int j = 0; j < kRuns; ++j)
-          if (j < kTile / kStep || key0 + kStep * j < kTile)
-            cp_async16((j & 1 ? to_odd : to) + j * (kStep * 128), src + static_cast<int64_t>(max(row[j], 0)) * (2 * kRow),
-                       row[j] >= 0 ? 16 : 0);
+          cp_async16(to + j * (kStep * 128), src + static_cast<int64_t>(max(row[j], 0)) * (2 * kRow), row[j] >= 0 ? 16 : 0);
         cp_async_arrive(&ms.pair_full[sl]);
         ++pairs;
       }
@@ -271,9 +300,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       const uint8_t* src = from + 2 * kLat + (lane & 7) * 16;
 #pragma unroll
       for (int j = 0; j < kRopeRuns; ++j)
-        if (j < kTile / kRopeStep || key1 + kRopeStep * j < kTile)
-          cp_async16(to + j * (kRopeStep * 128), src + static_cast<int64_t>(max(rope_row[j], 0)) * (2 * kRow),
-                     rope_row[j] >= 0 ? 16 : 0);
+        cp_async16(to + j * (kRopeStep * 128), src + static_cast<int64_t>(max(rope_row[j], 0)) * (2 * kRow),
+                   rope_row[j] >= 0 ? 16 : 0);
       cp_async_arrive(&ms.rope_full[sl]);
       ++ropes;
       ++tiles;
@@ -314,6 +342,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         tmem_ld<NC>(s_addr, r);
         tmem_wait();
         regs_ready<NC>(r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.s_free);
         float z[NC];                                       // scores, then their logarithms' distances from m
 #pragma unroll
         for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(r[c]);
@@ -360,7 +391,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < NC; ++c) l[c] *= ms.alpha[sw][c];
-          if (t > pc.t0) {                                 // (the scores' arrival implies the last product's end)
+          if (t > pc.t0) {
+            if (!(ok = waits(&ms.p_free, (tiles - 1) & 1))) break;   // the last product has ended
+            tc_fence_after();
 #pragma unroll 1
             for (int blk = 0; blk < 4; ++blk) {
               uint32_t o[NC];
@@ -375,10 +408,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
             tmem_wait_st();
           }
         }
-        // P row of this key: NC bf16, 128-byte swizzle
+        // P row of this key: NC bf16, 128-byte swizzle, once the last product has read its P
+        uint32_t w[NC / 2];
 #pragma unroll
         for (int c = 0; c < NC; c += 8) {
-          uint32_t w[4];
           const float4 m0 = *reinterpret_cast<const float4*>(&ms.m[sw][c]);
           const float4 m1 = *reinterpret_cast<const float4*>(&ms.m[sw][c + 4]);
           const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
@@ -386,12 +419,16 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
           for (int e = 0; e < 4; ++e) {
             const float p0 = ex2(fmaf(z[c + 2 * e], scale, -mm[2 * e]));
             const float p1 = ex2(fmaf(z[c + 2 * e + 1], scale, -mm[2 * e + 1]));
-            w[e] = bf_pack_weights(p0, p1);
+            w[c / 2 + e] = bf_pack_weights(p0, p1);
             l[c + 2 * e] += p0;
             l[c + 2 * e + 1] += p1;
           }
-          *reinterpret_cast<uint4*>(p_row + (((part_id * NC + c) / 8) ^ (key & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        if (tiles >= 1 && !(ok = waits(&ms.p_free, (tiles - 1) & 1))) break;
+#pragma unroll
+        for (int c = 0; c < NC / 8; ++c)
+          *reinterpret_cast<uint4*>(p_row + ((part_id * NC / 8 + c) ^ (key & 7)) * 16) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         // a draft's row that only some columns see must not reach the others as
         // 0 · NaN: where it is not finite it becomes zero (the columns that see
         // it have it in their weights already)
