@@ -352,35 +352,69 @@ def sparse_mla_decode(q, kv, indices, softmax_scale: float, out=None, stream=Non
     return out
 
 
-def _same_device(what: str, **tensors):
-    """The one CUDA device that all the tensors (None: absent) are on."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise IdxError(f"{what}: {name} must be a CUDA tensor")
-        if dev is not None and t.device != dev:
-            raise IdxError(f"{what}: {name} is on {t.device}, other arguments on {dev}")
-        dev = t.device
-    return dev
-
-
-def _typed(what: str, name: str, t, dtype, shape):
-    if t is None:
-        return
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise IdxError(f"{what}: {name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+def _refuse(what: str, name: str, t, dtypes, shape, dev: int, strided: bool):
+    """Raise for the first thing that is wrong with an argument of a paged call."""
+    if t.dtype not in dtypes:
+        raise IdxError(f"{what}: {name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.shape != shape:
         raise ValueError(f"{what}: {name} has shape {list(t.shape)}, expected {list(shape)}")
+    if t.get_device() != dev:
+        raise IdxError(f"{what}: {name} is on {t.device}, other arguments are not")
+    raise IdxError(f"{what}: {name} must be contiguous" + (" in its last dimension" if strided else ""))
 
 
-def _pitches(what: str, name: str, t):
-    """Element pitches of all dimensions but the last, which must be contiguous;
-    a dimension of one entry has no pitch (0)."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise IdxError(f"{what}: {name}'s last dimension must be contiguous")
-    return [0 if t.shape[d] <= 1 else t.stride(d) for d in range(t.dim() - 1)]
+def _args(what: str, dev: int, *args):
+    """Data pointers of (name, tensor or None, dtypes, shape) arguments, all of them
+    contiguous and on CUDA device `dev`.  One short test per tensor: a decode step
+    makes these calls once per layer."""
+    out = []
+    for name, t, dtypes, shape in args:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype not in dtypes or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+            _refuse(what, name, t, dtypes, shape, dev, False)
+        out.append(t.data_ptr())
+    if dev < 0:
+        raise IdxError(f"{what}: the arguments must be CUDA tensors")
+    return out
+
+
+class _On:
+    """The device of a call's tensors as the current one, and its stream (None: the
+    device's current stream) as the current one for what the call allocates;
+    .stream is its handle.  Does nothing where both are so already."""
+
+    __slots__ = ("device", "given", "stream", "contexts")
+
+    def __init__(self, device: int, stream):
+        self.device, self.given, self.contexts = device, stream, ()
+
+    def __enter__(self):
+        contexts = []
+        if torch.cuda.current_device() != self.device:
+            contexts.append(torch.cuda.device(self.device))
+        if self.given is not None:
+            if self.given.device.index != self.device:
+                raise IdxError(f"the stream is on cuda:{self.given.device.index}, the tensors on cuda:{self.device}")
+            contexts.append(torch.cuda.stream(self.given))
+        for c in contexts:
+            c.__enter__()
+        self.contexts = contexts
+        self.stream = torch._C._cuda_getCurrentRawStream(self.device)
+        return self
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+        return False
+
+
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_BITS64 = (torch.int64, torch.uint64)
+_OUT = (torch.bfloat16, torch.float32)
+_U8 = (torch.uint8,)
 
 
 def latent_append(kv_proj, gain, eps: float, rope_cos, rope_sin, positions, page_table, cache, *,
@@ -395,39 +429,42 @@ def latent_append(kv_proj, gain, eps: float, rope_cos, rope_sin, positions, page
     512 … 575 of q_out [B, n, H, 576] bf16 (allocated when None; its other
     features are then unset).  Returns q_out."""
     what = "latent_append"
-    if kv_proj.dim() != 3 or cache.dim() != 3 or page_table.dim() != 2:
+    if kv_proj.dim() != 3 or cache.dim() != 3 or page_table.dim() != 2 or (q_pe is not None and q_pe.dim() != 4):
         raise ValueError("latent_append: kv_proj [B, n, 576], cache [num_pages, page_size, 576], "
-                         "page_table [B, max_pages]")
-    B, n = kv_proj.shape[:2]
-    row = LATENT + ROTARY
-    H = 0
-    if q_pe is not None:
-        if q_pe.dim() != 4:
-            raise ValueError("latent_append: q_pe [B, n, H, 64]")
-        H = q_pe.shape[2]
-    elif q_out is not None:
+                         "page_table [B, max_pages], q_pe [B, n, H, 64]")
+    if q_pe is None and q_out is not None:
         raise ValueError("latent_append: q_out without q_pe")
-    for name, t, dtype, shape in (
-            ("kv_proj", kv_proj, _BF16, (B, n, row)), ("gain", gain, torch.float32, (LATENT,)),
-            ("rope_cos", rope_cos, torch.float32, (B, n, ROTARY // 2)),
-            ("rope_sin", rope_sin, torch.float32, (B, n, ROTARY // 2)), ("positions", positions, torch.int32, (B,)),
-            ("counts", counts, torch.int32, (B,)), ("page_table", page_table, torch.int32, (B, page_table.shape[1])),
-            ("cache", cache, _BF16, (cache.shape[0], cache.shape[1], row)),
-            ("q_pe", q_pe, _BF16, (B, n, H, ROTARY)), ("q_out", q_out, _BF16, (B, n, H, row))):
-        _typed(what, name, t, dtype, shape)
-    dev = _same_device(what, kv_proj=kv_proj, gain=gain, rope_cos=rope_cos, rope_sin=rope_sin, positions=positions,
-                       counts=counts, page_table=page_table, cache=cache, q_pe=q_pe, q_out=q_out)
-    kb, kt = _pitches(what, "kv_proj", kv_proj)
-    qb, qt, qh = _pitches(what, "q_pe", q_pe) if q_pe is not None else (0, 0, 0)
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        if q_pe is not None and q_out is None:
-            q_out = torch.empty((B, n, H, row), dtype=torch.bfloat16, device=dev)
-        _check(load().idx_latent_append(
-            kv_proj.data_ptr(), kb, kt, _ptr(gain, name="gain"), float(eps), _ptr(rope_cos, name="rope_cos"),
-            _ptr(rope_sin, name="rope_sin"), int(bool(interleaved)), _ptr(positions, name="positions"),
-            _ptr(counts, name="counts"), _ptr(page_table, name="page_table"), page_table.shape[1], B, n,
-            _ptr(cache, name="cache"), cache.shape[0], cache.shape[1], q_pe.data_ptr() if H else None, qb, qt, qh, H,
-            _ptr(q_out, name="q_out") if H else None, _stream(stream)), "idx_latent_append")
+    B, n = kv_proj.shape[:2]
+    pages, page_size, max_pages = cache.shape[0], cache.shape[1], page_table.shape[1]
+    row = LATENT + ROTARY
+    H = 0 if q_pe is None else q_pe.shape[2]
+    dev = kv_proj.get_device()
+    tables = (B, n, ROTARY // 2)
+    # the two strided arguments: element pitches, 0 for a dimension of one entry
+    if kv_proj.dtype not in _BF16 or kv_proj.shape != (B, n, row) or kv_proj.stride(2) != 1:
+        _refuse(what, "kv_proj", kv_proj, _BF16, (B, n, row), dev, True)
+    kb, kt = kv_proj.stride(0) if B > 1 else 0, kv_proj.stride(1) if n > 1 else 0
+    qp, qb, qt, qh = None, 0, 0, 0
+    if q_pe is not None:
+        if q_pe.dtype not in _BF16 or q_pe.shape != (B, n, H, ROTARY) or q_pe.stride(3) != 1 or \
+                q_pe.get_device() != dev:
+            _refuse(what, "q_pe", q_pe, _BF16, (B, n, H, ROTARY), dev, True)
+        if H:
+            qp, qh = q_pe.data_ptr(), q_pe.stride(2) if H > 1 else 0
+            qb, qt = q_pe.stride(0) if B > 1 else 0, q_pe.stride(1) if n > 1 else 0
+    g, cos, sin, pos, cnt, tab, c, qo = _args(
+        what, dev, ("gain", gain, _F32, (LATENT,)), ("rope_cos", rope_cos, _F32, tables),
+        ("rope_sin", rope_sin, _F32, tables), ("positions", positions, _I32, (B,)), ("counts", counts, _I32, (B,)),
+        ("page_table", page_table, _I32, (B, max_pages)), ("cache", cache, _BF16, (pages, page_size, row)),
+        ("q_out", q_out, _BF16, (B, n, H, row)))
+    with _On(dev, stream) as on:
+        if H and q_out is None:
+            q_out = torch.empty((B, n, H, row), dtype=torch.bfloat16, device=kv_proj.device)
+            qo = q_out.data_ptr()
+        code = load().idx_latent_append(kv_proj.data_ptr(), kb, kt, g, eps, cos, sin, 1 if interleaved else 0, pos, cnt, tab, max_pages,
+                                        B, n, c, pages, page_size, qp, qb, qt, qh, H, qo if H else None, on.stream)
+    if code:
+        _check(code, "idx_latent_append")
     return q_out
 
 
@@ -446,43 +483,49 @@ def tree_mla(q, cache, page_table, lengths, softmax_scale: float, *, max_len: in
     (None: a chain).  indices [B, n, k] int32: the context positions each row
     attends to (None: the whole context).  out bf16 or fp32 (allocated as bf16 when
     None, its rows behind the counts unset), ws: uint8 workspace of
-    tree_mla_workspace_size bytes (allocated on the stream when None)."""
+    tree_mla_workspace_size bytes (allocated on the stream when None; calls that
+    may overlap, captured graphs among them, need one each)."""
     what = "tree_mla"
     if q.dim() != 4 or cache.dim() != 3 or page_table.dim() != 2 or (indices is not None and indices.dim() != 3):
         raise ValueError("tree_mla: q [B, n, H, 576], cache [num_pages, page_size, 576], page_table [B, max_pages], "
                          "indices [B, n, k]")
     B, n, H = q.shape[:3]
-    row = LATENT + ROTARY
     if n > MAX_DRAFTS:
         raise ValueError(f"tree_mla: at most {MAX_DRAFTS} rows per sequence")
-    k = indices.shape[2] if indices is not None else 0
-    if indices is not None and k == 0:
-        raise ValueError("tree_mla: indices of width 0 (pass None for the whole context)")
-    for name, t, dtype, shape in (
-            ("q", q, _BF16, (B, n, H, row)), ("cache", cache, _BF16, (cache.shape[0], cache.shape[1], row)),
-            ("page_table", page_table, torch.int32, (B, page_table.shape[1])), ("lengths", lengths, torch.int32, (B,)),
-            ("counts", counts, torch.int32, (B,)), ("tree_mask", tree_mask, (torch.int64, torch.uint64), (B, n)),
-            ("indices", indices, torch.int32, (B, n, k)),
-            ("out", out, (torch.bfloat16, torch.float32), (B, n, H, LATENT)),
-            ("lse", lse, torch.float32, (B, n, H))):
-        _typed(what, name, t, dtype, shape)
-    dev = _same_device(what, q=q, cache=cache, page_table=page_table, lengths=lengths, counts=counts,
-                       tree_mask=tree_mask, indices=indices, out=out, lse=lse, ws=ws)
-    with torch.cuda.device(dev), torch.cuda.stream(stream):     # what is allocated here belongs to the call's stream
+    pages, page_size, max_pages = cache.shape[0], cache.shape[1], page_table.shape[1]
+    row = LATENT + ROTARY
+    k = 0
+    if indices is not None:
+        k = indices.shape[2]
+        if k == 0:
+            raise ValueError("tree_mla: indices of width 0 (pass None for the whole context)")
+    if ws is not None and (ws.dtype != torch.uint8 or ws.dim() != 1):
+        raise ValueError("tree_mla: ws is a one-dimensional uint8 tensor")
+    dev = q.get_device()
+    qp, c, tab, ln, cnt, mask, idx, op, lp, wp = _args(
+        what, dev, ("q", q, _BF16, (B, n, H, row)), ("cache", cache, _BF16, (pages, page_size, row)),
+        ("page_table", page_table, _I32, (B, max_pages)), ("lengths", lengths, _I32, (B,)),
+        ("counts", counts, _I32, (B,)), ("tree_mask", tree_mask, _BITS64, (B, n)), ("indices", indices, _I32, (B, n, k)),
+        ("out", out, _OUT, (B, n, H, LATENT)), ("lse", lse, _F32, (B, n, H)),
+        ("ws", ws, _U8, None if ws is None else ws.shape))
+    lib = load()
+    with _On(dev, stream) as on:                 # what is allocated here belongs to the call's stream
         if out is None:
-            out = torch.empty((B, n, H, LATENT), dtype=torch.bfloat16, device=dev)
+            out = torch.empty((B, n, H, LATENT), dtype=torch.bfloat16, device=q.device)
+            op = out.data_ptr()
         if lse is None:
-            lse = torch.empty((B, n, H), dtype=torch.float32, device=dev)
+            lse = torch.empty((B, n, H), dtype=torch.float32, device=q.device)
+            lp = lse.data_ptr()
         if ws is None:
-            need = tree_mla_workspace_size(B, n, H, max_len, k)
-            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _check(load().idx_tree_mla(
-            _ptr(q, name="q"), _ptr(cache, name="cache"), _ptr(page_table, name="page_table"), page_table.shape[1],
-            cache.shape[0], cache.shape[1], _ptr(lengths, name="lengths"), _ptr(counts, name="counts"), B, n, H,
-            max_len, _ptr(tree_mask, name="tree_mask"), _ptr(indices, name="indices") if k else None, k,
-            float(softmax_scale), _ptr(out, name="out"), OUT_BF16 if out.dtype == torch.bfloat16 else OUT_F32,
-            _ptr(lse, name="lse"), _ptr(ws, name="ws"), 0 if ws is None else ws.numel() * ws.element_size(),
-            _stream(stream)), "idx_tree_mla")
+            need = lib.idx_tree_mla_workspace_size(B, n, H, max_len, k)
+            if need:
+                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+                wp = ws.data_ptr()
+        code = lib.idx_tree_mla(qp, c, tab, max_pages, pages, page_size, ln, cnt, B, n, H, max_len, mask, idx, k,
+                                softmax_scale, op, OUT_BF16 if out.dtype is torch.bfloat16 else OUT_F32, lp, wp,
+                                0 if ws is None else ws.numel(), on.stream)
+    if code:
+        _check(code, "idx_tree_mla")
     return out, lse
 
 
