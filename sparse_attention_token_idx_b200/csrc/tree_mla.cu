@@ -518,75 +518,72 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
 
 // Joins the pieces of the items that shares cut: CTA (x, y) takes every kJoinY-th
 // run of outputs of the item that begins in CTA x's share and goes on in the next
-// teams'.  A thread ↔ four output features of a row, walking the pieces with a
+// teams'.  A thread ↔ eight output features of a row, walking the pieces with a
 // running maximum; many pieces (one long sequence) are split over four threads,
 // whose results are added in a fixed order.  Reads what the pieces wrote, from L2.
-constexpr int kJoinThreads = 256, kJoinY = 16;
+constexpr int kJoinThreads = 256, kJoinY = 8;
+struct Joined {
+  float o[8], top, z;
+};
+__device__ __forceinline__ void join_add(Joined& a, float m, float z, const float* x) {
+  const float up = fmaxf(a.top, m), base = up == -INFINITY ? 0.f : up;
+  const float keep = ex2(a.top - base), w = ex2(m - base);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a.o[i] = a.o[i] * keep + w * x[i];
+  a.z = a.z * keep + w * z;
+  a.top = up;
+}
 __global__ void __launch_bounds__(kJoinThreads) tree_mla_join_kernel(const TreeParams p) {
-  __shared__ float4 acc[kJoinThreads];
-  __shared__ float2 stat[kJoinThreads];
+  __shared__ Joined part[kJoinThreads];
   const Cut cut = p.cuts[blockIdx.x];
   if (!cut.pieces) return;
-  const int D = kLat / p.halves, D4 = D / 4;   // output features per slot row
+  const int D = kLat / p.halves, D8 = D / 8;   // output features per slot row
   const int split = cut.pieces >= 8 ? 4 : 1, width = kJoinThreads / split;
   const int group = threadIdx.x / width, id = threadIdx.x % width;
   const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
   const int64_t stride = static_cast<int64_t>(p.halves) * 2 * p.M * (D + 2);
   const float* next = part_slot(p, static_cast<int64_t>(team) * p.halves + rank, 0);   // slot 0 of this team
   const float* first = part_slot(p, static_cast<int64_t>(team) * p.halves + rank, 1);
-  for (int e0 = blockIdx.y * width; e0 < cut.rows * D4; e0 += kJoinY * width) {
-    const int e = min(e0 + id, cut.rows * D4 - 1), c = e / D4, d = e % D4;
+  const int count = cut.rows * D8;
+  for (int e0 = blockIdx.y * width; e0 < count; e0 += kJoinY * width) {
+    // neighbours in memory are neighbours in the CTA: features of a row, or rows
+    const int e = min(e0 + id, count - 1);
+    const int c = p.halves == 1 ? e / D8 : e % cut.rows, d = p.halves == 1 ? e % D8 : e / cut.rows;
+    const int at = p.halves == 1 ? c * D + d * 8 : (d * p.M + c) * 8;
     const int at_m = p.M * D + c, at_z = at_m + p.M;
-    float top = -INFINITY, z = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    Joined a{{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, -INFINITY, 0.f};
 #pragma unroll 4
     for (int i = group; i <= cut.pieces; i += split) {
       const float* s = i == 0 ? first : next + i * stride;   // piece 0: this team's slot 1; then the next teams' slot 0
-      const float m = s[at_m], zi = s[at_z];
-      const float4 x = *reinterpret_cast<const float4*>(s + c * D + d * 4);
-      const float up = fmaxf(top, m), base = up == -INFINITY ? 0.f : up;
-      const float a = ex2(top - base), w = ex2(m - base);
-      o.x = o.x * a + w * x.x;
-      o.y = o.y * a + w * x.y;
-      o.z = o.z * a + w * x.z;
-      o.w = o.w * a + w * x.w;
-      z = z * a + w * zi;
-      top = up;
+      const float m = s[at_m], z = s[at_z];
+      const float4 x0 = *reinterpret_cast<const float4*>(s + at), x1 = *reinterpret_cast<const float4*>(s + at + 4);
+      const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      join_add(a, m, z, x);
     }
     if (split > 1) {
-      acc[threadIdx.x] = o;
-      stat[threadIdx.x] = make_float2(top, z);
+      part[threadIdx.x] = a;
       __syncthreads();
-      if (group == 0) {
-        float up = top;
-        for (int g = 1; g < split; ++g) up = fmaxf(up, stat[g * width + id].x);
-        const float base = up == -INFINITY ? 0.f : up;
-        z = 0.f;
-        o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int g = 0; g < split; ++g) {
-          const float4 x = acc[g * width + id];
-          const float2 mz = stat[g * width + id];
-          const float w = ex2(mz.x - base);
-          o.x += w * x.x;
-          o.y += w * x.y;
-          o.z += w * x.z;
-          o.w += w * x.w;
-          z += w * mz.y;
+      if (group == 0)
+        for (int g = 1; g < split; ++g) {
+          const Joined& b = part[g * width + id];
+          join_add(a, b.top, b.z, b.o);
         }
-        top = up;
-      }
       __syncthreads();
     }
-    if (group == 0 && e0 + id < cut.rows * D4) {
-      const float inv = z == 0.f ? 0.f : 1.f / z;
-      const int64_t at = (cut.row0 + c) * kLat + rank * D + d * 4;
-      if (p.out_bf16)
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-            make_uint2(bf_pack(o.x * inv, o.y * inv), bf_pack(o.z * inv, o.w * inv));
-      else
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      if (p.lse && d == 0 && rank == 0) p.lse[cut.row0 + c] = lse_of(top, z);
+    if (group == 0 && e0 + id < count) {
+      const float inv = a.z == 0.f ? 0.f : 1.f / a.z;
+      const int64_t to = (cut.row0 + c) * kLat + rank * D + d * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a.o[i] *= inv;
+      if (p.out_bf16) {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to) =
+            make_uint4(bf_pack(a.o[0], a.o[1]), bf_pack(a.o[2], a.o[3]), bf_pack(a.o[4], a.o[5]), bf_pack(a.o[6], a.o[7]));
+      } else {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + to);
+        dst[0] = make_float4(a.o[0], a.o[1], a.o[2], a.o[3]);
+        dst[1] = make_float4(a.o[4], a.o[5], a.o[6], a.o[7]);
+      }
+      if (p.lse && d == 0 && rank == 0) p.lse[cut.row0 + c] = lse_of(a.top, a.z);
     }
   }
 }

@@ -530,7 +530,8 @@ __device__ __forceinline__ float lse_of(float m, float z) {    // m in log2 unit
   return m == -INFINITY && z == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * kLn2) + logf(z);
 }
 
-// partial slot of a CTA: M rows of D outputs, M maxima, M sums
+// partial slot of a CTA: M rows of D outputs (as [M][D], in runs of eight as
+// [D / 8][M][8] where a row's outputs are split over two CTAs), M maxima, M sums
 __device__ __forceinline__ float* part_slot(const TreeParams& p, int64_t cta, int slot) {
   return p.part + (cta * 2 + slot) * (static_cast<int64_t>(p.M) * (kLat / p.halves + 2));
 }

@@ -60,7 +60,8 @@ static_assert(kColS + kKeys <= kColO, "TMEM columns");
 
 struct WideState : PlanState<kRows, kKeys, kThreads / 32> {
   float top[2][kRows], sum[2][kRows];         // per half of the keys
-  uint64_t v_full[kVs], v_empty[kVs], x_full[2], x_done;
+  uint64_t v_full[kVs], v_empty[kVs], x_full[2];
+  uint64_t x_head, x_tail[2];                 // scores: the first three chunks done, all five
   uint64_t q_ready, s_full, s_free, p_full, p_free, o_full, o_free, drain_bar[2];
 };
 constexpr int kSmem = 1024 + kOffMisc + static_cast<int>(sizeof(WideState));
@@ -88,7 +89,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ms.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&ms.x_full[i], kCopyWarps * 32);
-    mbar_init(&ms.x_done, 1);
+    mbar_init(&ms.x_head, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ms.x_tail[i], 1);
     mbar_init(&ms.q_ready, kSoftWarps);
     mbar_init(&ms.s_full, 1);
     mbar_init(&ms.s_free, kSoftWarps);
@@ -144,9 +146,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b = k_desc + static_cast<uint64_t>((kOffX >> 4) + x * (kChunk >> 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + u * 32 + i * 8, b + i * 2, id_s, (u > 0 || i > 0) ? 1u : 0u);
+            if (u == 2) mma_commit(&ms.x_head);
             x = x == kXs - 1 ? 0 : x + 1;
           }
-          mma_commit(&ms.x_done);
+          mma_commit(&ms.x_tail[tiles & 1]);
           const uint64_t b = k_desc + static_cast<uint64_t>(sl * (kV >> 4));
 #pragma unroll
           for (int i = 0; i < 4; ++i) mma_f16_ta(d_s, tmem + 5 * 32 + i * 8, b + i * 2, id_s, 1u);
@@ -239,11 +242,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 2; ++j) xrow[j] = ms.row[par][key1 + 32 * j];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.tile_read[par]);
-      // chunk 5·t + u takes the place of the one seven earlier: of tile t − 2 for
-      // the first two (waited for at tile t − 1), of tile t − 1 for the others
+      // chunk 5·t + u takes the place of the one seven earlier: the last two of tile
+      // t − 2, then the first three of tile t − 1
 #pragma unroll
       for (int u = 0; u < 5; ++u) {
-        if (u == 2 && tiles >= 1 && !(ok = waits.nap(&ms.x_done, (tiles - 1) & 1))) break;
+        if (u == 0 && tiles >= 2 && !(ok = waits.nap(&ms.x_tail[tiles & 1], ((tiles >> 1) - 1) & 1))) break;
+        if (u == 2 && tiles >= 1 && !(ok = waits.nap(&ms.x_head, (tiles - 1) & 1))) break;
         const uint8_t* src = from + feature_chunk(u, half) * 128 + (lane & 7) * 16;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -288,23 +292,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* p_row = smem + kOffP + r_id * 128;
     bool ok = true;
     int tiles = 0, pieces = 0;
-    // three of the six query chunks that live in TMEM, into this warp's lanes
+    // Three of the six query chunks that live in TMEM, into this warp's lanes: read
+    // as 64-byte runs of eight rows (a lane reading its own row would touch 32
+    // lines per instruction), turned through the warp's 2 KB of the P buffer, which
+    // the last product must have left
+    uint8_t* stage = smem + kOffP + sw * 2048;
     auto load_q = [&](const Piece& pc) {
+      const int r0 = quad * 32 + (lane >> 2), pc16 = lane & 3;
+      const uint16_t* src = p.q + (pc.row0 + r0) * kRow + pc16 * 8;
 #pragma unroll 1
-      for (int i = 0; i < 3; ++i) {
-        const int pos = part * 3 + i;
-        uint32_t r[32];
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (pc.row0 + r_id) * kRow + feature_chunk(pos, half) * 64);
+      for (int h = 0; h < 6; h += 3) {
+        uint4 x[3][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 x = r_id < pc.rows ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-          r[4 * j] = x.x;
-          r[4 * j + 1] = x.y;
-          r[4 * j + 2] = x.z;
-          r[4 * j + 3] = x.w;
+        for (int k = 0; k < 3; ++k) {
+          const int f = feature_chunk(part * 3 + (h + k) / 2, half) * 64 + ((h + k) & 1) * 32;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[k][j] = r0 + 8 * j < pc.rows ? __ldg(reinterpret_cast<const uint4*>(src + 8 * j * kRow + f)) : make_uint4(0, 0, 0, 0);
         }
-        tmem_st<16>(lanes + pos * 32, r);
-        tmem_st<16>(lanes + pos * 32 + 16, r + 16);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = (lane >> 2) + 8 * j;
+            *reinterpret_cast<uint4*>(stage + r * 64 + ((pc16 ^ (r >> 1)) & 3) * 16) = x[k][j];
+          }
+          __syncwarp();
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + lane * 64 + ((j ^ (lane >> 1)) & 3) * 16);
+            w[4 * j] = y.x;
+            w[4 * j + 1] = y.y;
+            w[4 * j + 2] = y.z;
+            w[4 * j + 3] = y.w;
+          }
+          tmem_st<16>(lanes + (part * 3 + (h + k) / 2) * 32 + ((h + k) & 1) * 16, w);
+          __syncwarp();
+        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -437,9 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&ms.p_full);
       }
       if (!ok) break;
-      // ---- the next piece's queries, under the last product
+      // ---- the next piece's queries, once the last product has read P
       const int nb = pb ^ 1;
       if (!(ok = waits(&ms.piece_full[nb], ((pieces + 1) >> 1) & 1))) break;
+      if (!(ok = waits(&ms.o_full, pieces & 1))) break;
       if (ms.piece[nb].t0 != ms.piece[nb].t1) load_q(ms.piece[nb]);
       // ---- the sum over all keys, and this thread's 128 outputs
       ms.sum[part][r_id] = l;
@@ -456,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float inv = whole ? (z == 0.f ? 0.f : 1.f / z) : 1.f;
-      if (!(ok = waits(&ms.o_full, pieces & 1))) break;
       tc_fence_after();
       const int64_t at = (pc.row0 + r_id) * kLat + half * kHalf + part * (kHalf / 2);
+      float* mine = slot + (part * (kHalf / 2) * kRows + r_id * 8);   // [output / 8][row][8]: a warp's rows lie together
 #pragma unroll 1
       for (int q = 0; q < kHalf / 2; q += 16) {
         uint32_t o[16];
@@ -468,11 +494,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!have) {
           // (the loads are for all lanes)
         } else if (!whole || !p.out_bf16) {
-          float* dst = whole ? static_cast<float*>(p.out) + at + q : slot + r_id * kHalf + part * (kHalf / 2) + q;
+          float* dst = whole ? static_cast<float*>(p.out) + at + q : mine + q * kRows;
 #pragma unroll
           for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
           st_global32(dst, o);
-          st_global32(dst + 8, o + 8);
+          st_global32(dst + (whole ? 8 : 8 * kRows), o + 8);
         } else {
 #pragma unroll
           for (int c = 0; c < 8; ++c)
