@@ -55,7 +55,8 @@ struct Cfg {
   static constexpr int kSoftWarps = N == 64 ? 16 : 8;
   static constexpr int kParts = kSoftWarps / 4;             // row parts, each of four warps (128 keys)
   static constexpr int kNC = N / kParts;                    // rows per softmax thread
-  static constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
+  static constexpr int kPrefetchWarp = kFirstSoft + kSoftWarps;
+  static constexpr int kThreads = (kPrefetchWarp + 1) * 32;
   static constexpr int kPairs = N == 16 ? 5 : 4;            // latent buffers
   static constexpr int kRopes = N == 32 ? 2 : 1;            // rotary-chunk buffers
   static constexpr bool kAliasP = N == 64;                  // P takes the rotary chunk's place after the scores
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     mbar_init(&ms.o_full, 1);
     mbar_init(&ms.o_free, C::kSoftWarps);
     for (int i = 0; i < 2; ++i) mbar_init(&ms.drain_bar[i], 1);
-    ms.init(p.B, kCopyWarps + C::kSoftWarps, C::kSoftWarps + 2);
+    ms.init(p.B, kCopyWarps + C::kSoftWarps + 1, C::kSoftWarps + 2);
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
   }
@@ -307,6 +308,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       ++tiles;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");       // they have landed before the memory goes
+  } else if (warp == C::kPrefetchWarp) {
+    // ================================================================ prefetch
+    prefetch_tiles<kTile>(p, ms, waits, 0, 1, p.indices != nullptr);
   } else {
     // ================================================================ softmax
     constexpr int kColShift = NC == 16 ? 1 : 2;

@@ -526,6 +526,26 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
   if (pieces) waits.drain(&ms.q_full, (pieces - 1) & 1);   // landed before the memory goes
 }
 
+// A warp that asks for the tiles' 128-byte lines in L2, up to kAhead tiles before
+// their copies: its `part` of `parts`.
+template <int KT, class State>
+__device__ __forceinline__ void prefetch_tiles(const TreeParams& p, State& ms, const Waits& waits, int part, int parts,
+                                               bool ask) {
+  const int lane = threadIdx.x & 31;
+  const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
+  for (int tiles = 0;; ++tiles) {
+    const int at = tiles % kAhead;
+    if (!waits.nap(&ms.tile_full[at], (tiles / kAhead) & 1) || ms.last[at]) break;
+    if (ask)
+      for (int i = part * 32 + lane; i < KT * 9; i += 32 * parts) {
+        const int r = ms.row[at][i / 9];
+        if (r >= 0) prefetch_l2(from + static_cast<int64_t>(r) * (2 * kRow) + i % 9 * 128);
+      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ms.tile_read[at]);
+  }
+}
+
 __device__ __forceinline__ float lse_of(float m, float z) {    // m in log2 units
   return m == -INFINITY && z == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * kLn2) + logf(z);
 }

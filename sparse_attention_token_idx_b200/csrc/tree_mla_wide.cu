@@ -269,20 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");       // they have landed before the memory goes
   } else if (warp == kPrefetchWarp) {
     // ================================================================ prefetch
-    // the tiles' 128-byte lines into L2, up to kAhead tiles before their copies:
-    // each CTA of the team asks for its half
-    for (int tiles = 0;; ++tiles) {
-      const int par = tiles % kAhead;
-      if (!waits.nap(&ms.tile_full[par], (tiles / kAhead) & 1) || ms.last[par]) break;
-      const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
-#pragma unroll
-      for (int i = 0; i < kKeys * 9 / 64; ++i) {
-        const int line = i * 64 + half * 32 + lane, r = ms.row[par][line / 9];
-        if (r >= 0) prefetch_l2(from + static_cast<int64_t>(r) * (2 * kRow) + line % 9 * 128);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.tile_read[par]);
-    }
+    prefetch_tiles<kKeys>(p, ms, waits, half, 2, true);
   } else {
     // ================================================================ softmax
     const int sw = warp - kFirstSoft, quad = warp & 3, part = sw >> 2;
@@ -297,47 +284,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     // lines per instruction), turned through the warp's 2 KB of the P buffer, which
     // the last product must have left
     uint8_t* stage = smem + kOffP + sw * 2048;
-    auto load_q = [&](const Piece& pc) {
+    auto load_q = [&](const Piece& pc, uint64_t* p_left, uint32_t parity) {
       const int r0 = quad * 32 + (lane >> 2), pc16 = lane & 3;
       const uint16_t* src = p.q + (pc.row0 + r0) * kRow + pc16 * 8;
-#pragma unroll 1
-      for (int h = 0; h < 6; h += 3) {
-        uint4 x[3][4];
+      uint4 x[3][4];
+      auto fetch = [&](int h) {                            // half chunk h of six
+        const int f = feature_chunk(part * 3 + h / 2, half) * 64 + (h & 1) * 32;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int f = feature_chunk(part * 3 + (h + k) / 2, half) * 64 + ((h + k) & 1) * 32;
+        for (int j = 0; j < 4; ++j)
+          x[h % 3][j] = r0 + 8 * j < pc.rows ? __ldg(reinterpret_cast<const uint4*>(src + 8 * j * kRow + f)) : make_uint4(0, 0, 0, 0);
+      };
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            x[k][j] = r0 + 8 * j < pc.rows ? __ldg(reinterpret_cast<const uint4*>(src + 8 * j * kRow + f)) : make_uint4(0, 0, 0, 0);
+      for (int h = 0; h < 3; ++h) fetch(h);
+      if (p_left && !waits(p_left, parity)) return false;
+#pragma unroll
+      for (int h = 0; h < 6; ++h) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = (lane >> 2) + 8 * j;
+          *reinterpret_cast<uint4*>(stage + r * 64 + ((pc16 ^ (r >> 1)) & 3) * 16) = x[h % 3][j];
         }
+        if (h + 3 < 6) fetch(h + 3);
+        __syncwarp();
+        uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = (lane >> 2) + 8 * j;
-            *reinterpret_cast<uint4*>(stage + r * 64 + ((pc16 ^ (r >> 1)) & 3) * 16) = x[k][j];
-          }
-          __syncwarp();
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 y = *reinterpret_cast<const uint4*>(stage + lane * 64 + ((j ^ (lane >> 1)) & 3) * 16);
-            w[4 * j] = y.x;
-            w[4 * j + 1] = y.y;
-            w[4 * j + 2] = y.z;
-            w[4 * j + 3] = y.w;
-          }
-          tmem_st<16>(lanes + (part * 3 + (h + k) / 2) * 32 + ((h + k) & 1) * 16, w);
-          __syncwarp();
+        for (int j = 0; j < 4; ++j) {
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + lane * 64 + ((j ^ (lane >> 1)) & 3) * 16);
+          w[4 * j] = y.x;
+          w[4 * j + 1] = y.y;
+          w[4 * j + 2] = y.z;
+          w[4 * j + 3] = y.w;
         }
+        tmem_st<16>(lanes + (part * 3 + h / 2) * 32 + (h & 1) * 16, w);
+        __syncwarp();
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.q_ready);
+      return true;
     };
     ok = waits(&ms.piece_full[0], 0);
-    if (ok && ms.piece[0].t0 != ms.piece[0].t1) load_q(ms.piece[0]);
+    if (ok && ms.piece[0].t0 != ms.piece[0].t1) load_q(ms.piece[0], nullptr, 0);
     while (ok) {
       const int pb = pieces & 1;
       const Piece pc = ms.piece[pb];
@@ -465,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the next piece's queries, once the last product has read P
       const int nb = pb ^ 1;
       if (!(ok = waits(&ms.piece_full[nb], ((pieces + 1) >> 1) & 1))) break;
+      if (ms.piece[nb].t0 != ms.piece[nb].t1 && !(ok = load_q(ms.piece[nb], &ms.o_full, pieces & 1))) break;
       if (!(ok = waits(&ms.o_full, pieces & 1))) break;
-      if (ms.piece[nb].t0 != ms.piece[nb].t1) load_q(ms.piece[nb]);
       // ---- the sum over all keys, and this thread's 128 outputs
       ms.sum[part][r_id] = l;
       bar_named(1 + quad, 64);
@@ -486,24 +474,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t at = (pc.row0 + r_id) * kLat + half * kHalf + part * (kHalf / 2);
       float* mine = slot + (part * (kHalf / 2) * kRows + r_id * 8);   // [output / 8][row][8]: a warp's rows lie together
 #pragma unroll 1
-      for (int q = 0; q < kHalf / 2; q += 16) {
-        uint32_t o[16];
+      for (int q = 0; q < kHalf / 2; q += 32) {
+        uint32_t o[32];
         tmem_ld<16>(lanes + kColO + part * (kHalf / 2) + q, o);
+        tmem_ld<16>(lanes + kColO + part * (kHalf / 2) + q + 16, o + 16);
         tmem_wait();
-        regs_ready<16>(o);
+        regs_ready<32>(o);
         if (!have) {
           // (the loads are for all lanes)
         } else if (!whole || !p.out_bf16) {
           float* dst = whole ? static_cast<float*>(p.out) + at + q : mine + q * kRows;
+          const int next = whole ? 8 : 8 * kRows;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
-          st_global32(dst, o);
-          st_global32(dst + (whole ? 8 : 8 * kRows), o + 8);
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) st_global32(dst + c * next, o + 8 * c);
         } else {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at + q;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
+          for (int c = 0; c < 16; ++c)
             o[c] = bf_pack(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
-          st_global32(static_cast<__nv_bfloat16*>(p.out) + at + q, o);
+          st_global32(dst, o);
+          st_global32(dst + 16, o + 8);
         }
         __syncwarp();
       }
