@@ -62,7 +62,7 @@ struct WideState : PlanState<kRows, kKeys, kThreads / 32> {
   float top[2][kRows], sum[2][kRows];         // per half of the keys
   uint64_t v_full[kVs], v_empty[kVs], x_full[2];
   uint64_t x_head, x_tail[2];                 // scores: the first three chunks done, all five
-  uint64_t q_ready, s_full, s_free, p_full, p_free, o_full, o_free, drain_bar[2];
+  uint64_t q_ready, s_issued[2], s_full, s_free, p_full, p_free, o_full, o_free, drain_bar[2];
 };
 constexpr int kSmem = 1024 + kOffMisc + static_cast<int>(sizeof(WideState));
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ms.x_head, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&ms.x_tail[i], 1);
     mbar_init(&ms.q_ready, kSoftWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&ms.s_issued[i], 1);
     mbar_init(&ms.s_full, 1);
     mbar_init(&ms.s_free, kSoftWarps);
     mbar_init(&ms.p_full, kSoftWarps);
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         issued = true;
         __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.s_issued[tiles & 1]);   // (reaches the barrier as the queued MMAs drain)
         xs = (xs + 5) % kXs;
         ++tiles;
       }
@@ -192,11 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ms.piece_empty[pb]);
       if (n == 0) break;
       for (int c = 0; c < n; ++c) {
-        // O += P · V of tile c (its scores, and so its V, were complete before its P)
+        // O += P · V of tile c (its scores, and so its V, were complete before its P),
+        // behind the scores of tile c + 1: it then runs while the softmax reads those
+        // out of TMEM, when the tensor cores would wait for the buffer
         const int sl = tiles % kVs;
         if (c == 0 && pieces > 0 && !(ok = waits(&ms.o_free, (pieces - 1) & 1))) break;
         if (!(ok = waits(&ms.p_full, tiles & 1))) break;
-        fence_proxy_async_smem();
+        if (c < n - 1 && !(ok = waits(&ms.s_issued[(tiles + 1) & 1], ((tiles + 1) >> 1) & 1))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t b = v_desc + static_cast<uint64_t>(sl * (kV >> 4));
