@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c == 0 && pieces > 0 && !(ok = waits(&ms.o_free, (pieces - 1) & 1))) break;
         if (!(ok = waits(&ms.p_full, tiles & 1))) break;
         if (c < n - 1 && !(ok = waits(&ms.s_issued[(tiles + 1) & 1], ((tiles + 1) >> 1) & 1))) break;
+        fence_proxy_async_smem();              // P was written through the generic proxy
         tc_fence_after();
         if (elect_one()) {
           const uint64_t b = v_desc + static_cast<uint64_t>(sl * (kV >> 4));
@@ -246,21 +247,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 2; ++j) xrow[j] = ms.row[par][key1 + 32 * j];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.tile_read[par]);
-      // chunk 5·t + u takes the place of the one seven earlier: the last two of tile
-      // t − 2, then the first three of tile t − 1
-#pragma unroll
-      for (int u = 0; u < 5; ++u) {
-        if (u == 0 && tiles >= 2 && !(ok = waits.nap(&ms.x_tail[tiles & 1], ((tiles >> 1) - 1) & 1))) break;
-        if (u == 2 && tiles >= 1 && !(ok = waits.nap(&ms.x_head, (tiles - 1) & 1))) break;
+      // In the order in which places become free: chunk 5·t + u takes the place of
+      // the one seven earlier — the first two of tile t − 2's last two, the others of
+      // tile t − 1's first three, whose scores are the last thing to wait for — and V
+      // that of tile t − 3
+      auto copy_x = [&](int u) {
         const uint8_t* src = from + feature_chunk(u, half) * 128 + (lane & 7) * 16;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           cp_async16(to_x + xs * kChunk + j * 4096, src + static_cast<int64_t>(max(xrow[j], 0)) * (2 * kRow),
                      xrow[j] >= 0 ? 16 : 0);
         xs = xs == kXs - 1 ? 0 : xs + 1;
-      }
-      if (!ok) break;
-      cp_async_arrive(&ms.x_full[tiles & 1]);
+      };
+      if (tiles >= 2 && !(ok = waits.nap(&ms.x_tail[tiles & 1], ((tiles >> 1) - 1) & 1))) break;
+      copy_x(0);
+      copy_x(1);
       const int sl = tiles % kVs;
       if (tiles >= kVs && !(ok = waits.nap(&ms.v_empty[sl], (tiles / kVs - 1) & 1))) break;
       const uint8_t* src = from + half * 512 + lane * 16;
@@ -268,6 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 8; ++j)
         cp_async16(to_v + sl * kV + j * 1024, src + static_cast<int64_t>(max(row[j], 0)) * (2 * kRow), row[j] >= 0 ? 16 : 0);
       cp_async_arrive(&ms.v_full[sl]);
+      if (tiles >= 1 && !(ok = waits(&ms.x_head, (tiles - 1) & 1))) break;
+      copy_x(2);
+      copy_x(3);
+      copy_x(4);
+      cp_async_arrive(&ms.x_full[tiles & 1]);
       ++tiles;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");       // they have landed before the memory goes
@@ -336,20 +342,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pc.t0 == pc.t1) break;
       const uint64_t drafts = ms.mask[pb][r_id];
       float m = -INFINITY, l = 0.f;                        // reference maximum (log2 units), sum of this half's weights
-      for (int t = pc.t0; t < pc.t1; ++t, ++tiles) {
-        // what this row sees of the tile's keys: the context, and its drafts (draft
-        // j is key nkeys + j)
-        if (!(ok = waits(&ms.tile_full[tiles % kAhead], (tiles / kAhead) & 1))) break;
-        const int k0 = ms.kind[tiles % kAhead][part * 32 + lane];
-        const uint32_t ctx = __ballot_sync(0xFFFFFFFFu, k0 == 1), dr = __ballot_sync(0xFFFFFFFFu, k0 >= 2);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.tile_read[tiles % kAhead]);
-        uint32_t sees = ctx;
+      // what this row sees of a tile's keys: the context, and its drafts (draft j is
+      // key nkeys + j); read a tile ahead, while the last product runs
+      uint32_t next_sees = 0;
+      auto look = [&](int t, int tile) {
+        if (!waits(&ms.tile_full[tile % kAhead], (tile / kAhead) & 1)) return false;
+        const int kind = ms.kind[tile % kAhead][part * 32 + lane];
+        next_sees = __ballot_sync(0xFFFFFFFFu, kind == 1);
+        const uint32_t dr = __ballot_sync(0xFFFFFFFFu, kind >= 2);
         if (dr) {
           const int sh = pc.nkeys - (t * kKeys + part * 32);   // key of draft 0 in these 32
           const uint64_t at = sh >= 0 ? (sh < 64 ? drafts << sh : 0) : (sh > -64 ? drafts >> -sh : 0);
-          sees |= static_cast<uint32_t>(at) & dr;
+          next_sees |= static_cast<uint32_t>(at) & dr;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.tile_read[tile % kAhead]);
+        return true;
+      };
+      if (!(ok = look(pc.t0, tiles))) break;
+      for (int t = pc.t0; t < pc.t1; ++t, ++tiles) {
+        const uint32_t sees = next_sees;
         if (t == pc.t1 - 1 && waits.test(&ms.piece_full[pb ^ 1], ((pieces + 1) >> 1) & 1)) {
           const Piece& next = ms.piece[pb ^ 1];            // its queries into L2 (load_q reads them soon)
           if (next.t0 != next.t1 && r_id < next.rows)
@@ -401,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[c] = bf_pack_weights(p0, p1);
           l += p0 + p1;
         }
+        if (t + 1 < pc.t1 && !(ok = look(t + 1, tiles + 1))) break;
         // P and O are free once the last product has ended
         if (tiles >= 1 && !(ok = waits(&ms.p_free, (tiles - 1) & 1))) break;
         tc_fence_after();
@@ -448,7 +461,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 8; ++j) x[j] = make_uint4(0, 0, 0, 0);
           }
         }
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.p_full);
