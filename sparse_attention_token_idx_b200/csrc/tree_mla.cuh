@@ -324,6 +324,7 @@ struct Share {
 // CTA barriers; what was written before the first is visible after it.
 template <int M, int KT, int kThreads, class State>
 __device__ __forceinline__ Share find_share(const TreeParams& p, State& ms, int team) {
+  if (!p.whole) asm volatile("griddepcontrol.launch_dependents;");   // the join may be placed as SMs become free
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
@@ -529,18 +530,16 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
 // A warp that asks for the tiles' 128-byte lines in L2, up to kAhead tiles before
 // their copies: its `part` of `parts`.
 template <int KT, class State>
-__device__ __forceinline__ void prefetch_tiles(const TreeParams& p, State& ms, const Waits& waits, int part, int parts,
-                                               bool ask) {
+__device__ __forceinline__ void prefetch_tiles(const TreeParams& p, State& ms, const Waits& waits, int part, int parts) {
   const int lane = threadIdx.x & 31;
   const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
   for (int tiles = 0;; ++tiles) {
     const int at = tiles % kAhead;
     if (!waits.nap(&ms.tile_full[at], (tiles / kAhead) & 1) || ms.last[at]) break;
-    if (ask)
-      for (int i = part * 32 + lane; i < KT * 9; i += 32 * parts) {
-        const int r = ms.row[at][i / 9];
-        if (r >= 0) prefetch_l2(from + static_cast<int64_t>(r) * (2 * kRow) + i % 9 * 128);
-      }
+    for (int i = part * 32 + lane; i < KT * 9; i += 32 * parts) {
+      const int r = ms.row[at][i / 9];
+      if (r >= 0) prefetch_l2(from + static_cast<int64_t>(r) * (2 * kRow) + i % 9 * 128);
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms.tile_read[at]);
   }

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");       // they have landed before the memory goes
   } else if (warp == kPrefetchWarp) {
     // ================================================================ prefetch
-    prefetch_tiles<kKeys>(p, ms, waits, half, 2, true);
+    prefetch_tiles<kKeys>(p, ms, waits, half, 2);
   } else {
     // ================================================================ softmax
     const int sw = warp - kFirstSoft, quad = warp & 3, part = sw >> 2;
