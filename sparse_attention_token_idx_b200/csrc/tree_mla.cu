@@ -75,6 +75,7 @@ struct Misc : PlanState<N, kTile, Cfg<N>::kThreads / 32> {
   alignas(16) float sum[Cfg<N>::kParts][4][Cfg<N>::kNC];
   uint64_t pair_full[5], pair_empty[5], rope_full[2], rope_empty[2];
   uint64_t s_full, s_free, p_full, p_free, o_full, o_free, drain_bar[2];
+  int left_at[Cfg<N>::kParts];
 };
 
 // Column reduction of v[NC] over the warp's 32 lanes by a transposing butterfly;
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     mbar_init(&ms.o_full, 1);
     mbar_init(&ms.o_free, C::kSoftWarps);
     for (int i = 0; i < 2; ++i) mbar_init(&ms.drain_bar[i], 1);
+    for (int i = 0; i < C::kParts; ++i) ms.left_at[i] = 0;
     ms.init(p.B, kCopyWarps + C::kSoftWarps + (p.indices ? 1 : 0), C::kSoftWarps + 2);
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       for (int c = 0; c < n && ok; ++c) {
         // Sᵀ = K · qᵀ, once the softmax has read the last S, chunk by chunk as they land
         if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
+        if (p.fault && tiles == 1 && !(ok = waits(&ms.never, 0))) break;
         for (int u = 0; u < 4; ++u) {
           if (!(ok = waits(&ms.pair_full[slot], lap & 1))) break;
           fence_proxy_async_smem();                        // the copies wrote through the generic proxy
@@ -324,7 +327,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     const uint32_t s_addr = lanes + 4 * N + part_id * NC;
     const float scale = fmaxf(fabsf(p.scale_log2), 1.1754944e-38f);   // (never 0 · −inf)
     uint8_t* p_row = smem + C::kOffP + key * 128;
-    bool ok = true;
+    bool ok = true, gone = false;                          // gone: another warp of the part has given up
+    Meeting meeting{1 + part_id, 128, 0, &ms.left_at[part_id]};
     int tiles = 0, pieces = 0, pairs = 0;
     while (true) {
       const int pb = pieces & 1;
@@ -380,12 +384,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
           far = fmaxf(far, fmaxf(fmaf(z[c + 2], scale, -mc.z), fmaf(z[c + 3], scale, -mc.w)));
         }
         over |= far > kRaise;
-        if (bar_named_any(1 + part_id, 128, over)) {
+        if (meeting.vote(over)) {
+          if ((gone = meeting.left())) break;
           float v[NC];
 #pragma unroll
           for (int c = 0; c < NC; ++c) v[c] = z[c];
           ms.wmax[part_id][quad][my_col] = reduce_columns<NC, true>(v, lane);
-          bar_named(1 + part_id, 128);
+          meeting.vote(false);
           float top = ms.wmax[part_id][0][my_col];
 #pragma unroll
           for (int w = 1; w < 4; ++w) top = fmaxf(top, ms.wmax[part_id][w][my_col]);
@@ -464,10 +469,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.p_full);
       }
-      if (!ok) break;
+      if (!ok || gone) break;
       // ---- the sums over all keys
       ms.sum[part_id][quad][my_col] = reduce_columns<NC, false>(l, lane);
-      bar_named(1 + part_id, 128);
+      if (meeting.vote(false) && (gone = meeting.left())) break;
       float z = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) z += ms.sum[part_id][w][my_col];
@@ -515,6 +520,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       }
       ++pieces;
     }
+    if (!ok && !gone) meeting.leave();
   }
   // ------------------------------------------------------------ teardown
   tc_fence_before();
@@ -698,7 +704,9 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
   p.whole = pl.whole;
   p.part = static_cast<float*>(ws);
   p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(ws) + pl.part_bytes);
-  p.budget_ns = debug_state().budget_ns;
+  const DebugState dbg = debug_state();
+  p.budget_ns = dbg.budget_ns;
+  p.fault = dbg.flags & 1;
   p.err = device_error_word();
   if (!p.err) return check_launch();
   auto* s = reinterpret_cast<cudaStream_t>(stream);

@@ -65,6 +65,7 @@ struct TreeParams {
   float* part;                                // [CTA][2] partial slots: M · (512 / halves) outputs, M maxima, M sums
   Cut* cuts;                                  // [CTA]
   unsigned long long budget_ns;               // bound of every wait
+  int fault;                                  // tests: the second tile's scores wait for a barrier that nothing signals
   unsigned int* err;
 };
 
@@ -150,9 +151,6 @@ __device__ __forceinline__ uint32_t bf_pack_weights(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo) + 0x8000u, __float_as_uint(hi) + 0x8000u, 0x7632);
 }
 // `count` threads meet; whether any of them says v
-__device__ __forceinline__ void bar_named(int id, int count) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
 __device__ __forceinline__ bool bar_named_any(int id, int count, bool v) {
   uint32_t r;
   asm volatile(
@@ -162,6 +160,25 @@ __device__ __forceinline__ bool bar_named_any(int id, int count, bool v) {
       : "memory");
   return r != 0;
 }
+// The softmax warps that share rows meet at one named barrier, always by vote().
+// The meetings are not bounded in time, so a warp that gives up leaves: it writes
+// the number of the next meeting and takes its place there once more, saying true;
+// the others see the number and go too.  (A warp can give up only between
+// meetings that end a wait; the number tells this meeting from a later one.)
+struct Meeting {
+  int id, count, number;
+  volatile int* left_at;
+  __device__ __forceinline__ bool vote(bool v) {
+    ++number;
+    return bar_named_any(id, count, v);
+  }
+  __device__ __forceinline__ bool left() const { return __any_sync(0xFFFFFFFFu, *left_at == number); }
+  __device__ __forceinline__ void leave() {
+    *left_at = number + 1;
+    vote(true);
+  }
+};
+
 // A warp's wait for a phase of an mbarrier, for at most budget_ns; false once this
 // CTA has given up.  The global timer, whose read takes about 1 000 cycles, is
 // looked at every 256 polls only: a wait that succeeds at once costs some 60
@@ -292,6 +309,7 @@ struct PlanState {
   int start_b;
   int abort_flag;
   uint32_t tmem;
+  uint64_t never;                             // nothing signals it
   uint64_t tile_full[kAhead], tile_read[kAhead], piece_full[2], piece_empty[2], q_full, q_empty;
 
   __device__ void init(int B, int tile_readers, int piece_readers) {
@@ -303,6 +321,7 @@ struct PlanState {
       mbar_init(&piece_full[i], 1);
       mbar_init(&piece_empty[i], piece_readers);
     }
+    mbar_init(&never, 1);
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
     abort_flag = 0;

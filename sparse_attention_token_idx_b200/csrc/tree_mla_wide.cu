@@ -60,6 +60,7 @@ static_assert(kColS + kKeys <= kColO, "TMEM columns");
 
 struct WideState : PlanState<kRows, kKeys, kThreads / 32> {
   float top[2][kRows], sum[2][kRows];         // per half of the keys
+  int left_at[4];                             // per quarter of the rows
   uint64_t v_full[kVs], v_empty[kVs], x_full[2];
   uint64_t x_head, x_tail[2];                 // scores: the first three chunks done, all five
   uint64_t q_ready, s_issued[2], s_full, s_free, p_full, p_free, o_full, o_free, drain_bar[2];
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ms.o_full, 1);
     mbar_init(&ms.o_free, kSoftWarps);
     for (int i = 0; i < 2; ++i) mbar_init(&ms.drain_bar[i], 1);
+    for (int i = 0; i < 4; ++i) ms.left_at[i] = 0;
     ms.init(p.B, kCopyWarps + kSoftWarps + 1, kSoftWarps + 2);
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
@@ -139,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
         fence_proxy_async_smem();              // the copies wrote through the generic proxy
         if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
+        if (p.fault && tiles == 1 && !(ok = waits(&ms.never, 0))) break;
         tc_fence_after();
         if (elect_one()) {
           int x = xs;
@@ -287,7 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float scale = fmaxf(fabsf(p.scale_log2), 1.1754944e-38f);   // (never 0 · −inf)
     uint8_t* p_row = smem + kOffP + r_id * 128;
-    bool ok = true;
+    bool ok = true, gone = false;                          // gone: the other warp of these rows has given up
+    Meeting meeting{1 + quad, 64, 0, &ms.left_at[quad]};
     int tiles = 0, pieces = 0;
     // Three of the six query chunks that live in TMEM, into this warp's lanes: read
     // as 64-byte runs of eight rows (a lane reading its own row would touch 32
@@ -390,11 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c) far = fmaxf(far, z[c]);
         const float mu = m == -INFINITY ? kNone : m;
-        const bool raised = bar_named_any(1 + quad, 64, t == pc.t0 || fmaf(far, scale, -mu) > kRaise);
+        const bool raised = meeting.vote(t == pc.t0 || fmaf(far, scale, -mu) > kRaise);
         float a = 1.f;
         if (raised) {                                      // the same in both warps of these rows
+          if ((gone = meeting.left())) break;
           ms.top[part][r_id] = far;
-          bar_named(1 + quad, 64);
+          meeting.vote(false);
           float top = fmaxf(far, ms.top[1 - part][r_id]);
           top = top == -INFINITY ? top : top * scale;
           const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = top;
           }
           l *= a;
-          bar_named(1 + quad, 64);                         // (top may be written again)
+          meeting.vote(false);                             // (top may be written again)
         }
         const float base = m == -INFINITY ? kNone : m;
         uint32_t w[16];
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.p_full);
       }
-      if (!ok) break;
+      if (!ok || gone) break;
       // ---- the next piece's queries, once the last product has read P
       const int nb = pb ^ 1;
       if (!(ok = waits(&ms.piece_full[nb], ((pieces + 1) >> 1) & 1))) break;
@@ -473,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = waits(&ms.o_full, pieces & 1))) break;
       // ---- the sum over all keys, and this thread's 128 outputs
       ms.sum[part][r_id] = l;
-      bar_named(1 + quad, 64);
+      if (meeting.vote(false) && (gone = meeting.left())) break;
       const float z = ms.sum[0][r_id] + ms.sum[1][r_id];
       const bool whole = pc.slot < 0, have = r_id < pc.rows;
       float* slot = whole ? nullptr : part_slot(p, blockIdx.x, pc.slot);
@@ -523,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++pieces;
     }
+    if (!ok && !gone) meeting.leave();
   }
   // ------------------------------------------------------------ teardown
   tc_fence_before();

@@ -236,3 +236,118 @@ def test_streams_graphs_and_repeated_calls_agree():
     torch.cuda.synchronize()
     assert torch.equal(graphs[0][1], want2) and not torch.equal(want, want2)
     assert X.status() == (0, 0)
+
+
+@pytest.mark.parametrize("n,H,page,ctxs,cnts,k,tree", [
+    (1, 24, 64, [127, 128, 1000], None, 0, False),               # 17 to 32 rows per key set
+    (2, 16, 48, [0, 385, 64], [2, 1, 2], 0, True),
+    (2, 10, 16, [600, 100], None, 130, True),
+    (1, 64, 64, [3000, 1, 255], None, 0, False),                 # 33 to 64 rows
+    (4, 16, 33, [1000, 257], [4, 3], 0, True),
+    (1, 40, 100, [900], None, 300, False),
+    (1, 65, 64, [400, 63], None, 0, False),                      # one row more than the narrow kernels hold
+    (9, 16, 64, [700, 0], [9, 8], 0, True),                      # a second group of 128 rows for one sequence only
+    (1, 128, 64, [20000], None, 0, False),                       # one long sequence over the whole GPU, all heads
+    (2, 128, 16, [6000, 6001], None, 4000, True),                # many pieces of a selection
+])
+def test_row_counts_of_every_kernel(n, H, page, ctxs, cnts, k, tree):
+    from sparse_attention_token_idx_b200 import binding as X
+    rng = np.random.default_rng(n * 1000 + H + k + 1)
+    B = len(ctxs)
+    real = cnts or [n] * B
+    paged = Paged(rng, [a + m for a, m in zip(ctxs, real)], page).fill(rng)
+    q64, q = bf(rng.standard_normal((B, n, H, DIM)))
+    mask = [random_tree(rng, n) for _ in range(B)] if tree else None
+    idx = None
+    if k:
+        idx = np.full((B, n, k), -1, np.int32)
+        for b in range(B):
+            for i in range(n):
+                m = min(k, ctxs[b])
+                idx[b, i, :m] = rng.choice(ctxs[b], m, replace=False)
+    out, lse = _run(X, paged, q, real, n, mask, idx, given=cnts is not None)
+    check_tree(out, lse, q64, paged, real, SCALE, mask, idx, untouched=5.0)
+
+
+@pytest.mark.parametrize("H", [4, 30, 128])
+@pytest.mark.parametrize("scale", [3.0, -0.3])
+def test_reference_maximum_rises_in_every_kernel(H, scale):
+    """Scores that grow along a sequence cut into pieces, with peaky softmaxes."""
+    from sparse_attention_token_idx_b200 import binding as X
+    rng = np.random.default_rng(11)
+    L = 2500
+    paged = Paged(rng, [L, 700], 64).fill(rng)
+    for b in range(2):
+        for i in range(paged.lens[b]):
+            pg = paged.table[b, i // 64]
+            paged.cache[pg, i % 64], _ = bf(paged.cache[pg, i % 64] * (0.1 + 0.9 * i / L))
+    q64, q = bf(rng.standard_normal((2, 1, H, DIM)))
+    out, lse = _run(X, paged, q, [1, 1], 1, scale=scale)
+    check_tree(out, lse, q64, paged, [1, 1], scale)
+
+
+def test_large_batch_of_short_sequences_and_empty_batches():
+    """More sequences than a CTA has threads, without rows or a context here and
+    there; then a batch in which no sequence has a row."""
+    from sparse_attention_token_idx_b200 import binding as X
+    rng = np.random.default_rng(12)
+    B, n, H = 1300, 2, 3
+    cnts = [int(x) for x in rng.integers(0, 3, B)]
+    lens = [c + int(rng.integers(0, 40)) for c in cnts]
+    paged = Paged(rng, lens, 16).fill(rng)
+    q64, q = bf(rng.standard_normal((B, n, H, DIM)))
+    out, lse = _run(X, paged, q, cnts, n)
+    check_tree(out, lse, q64, paged, cnts, SCALE, untouched=5.0)
+    none = [0] * B
+    out, lse = _run(X, paged, q, none, n)
+    assert (out == 5).all() and (lse == 5).all()
+
+
+def test_pages_past_four_gigabytes():
+    """Cache rows whose byte offsets pass 32 bits, appended and attended to."""
+    from sparse_attention_token_idx_b200 import binding as X
+    rng = np.random.default_rng(13)
+    pages, page, H, L = 62000, 64, 16, 200
+    cache = torch.zeros((pages, page, DIM), dtype=torch.bfloat16, device="cuda")      # 4.6 GB
+    table = np.array([[pages - 1, pages - 3, 59000, pages - 2]], np.int32)
+    kv64, kv = bf(rng.standard_normal((1, L, DIM)))
+    gain, cos, sin = np.ones(LAT, np.float32), np.ones((1, L, 32), np.float32), np.zeros((1, L, 32), np.float32)
+    X.latent_append(kv.cuda(), dev(gain), 0.0, dev(cos), dev(sin), dev(np.zeros(1, np.int32)), dev(table), cache)
+    t = np.arange(L)
+    rows = cache[torch.from_numpy(table[0, t // page]).long().cuda(), torch.from_numpy(t % page).cuda()]
+    rms = np.sqrt(np.mean(kv64[0, :, :LAT] ** 2, axis=1, keepdims=True))
+    got = rows.double().cpu().numpy()
+    assert np.all(np.abs(got[:, :LAT] - kv64[0, :, :LAT] / rms) <= np.abs(kv64[0, :, :LAT] / rms) * (2 ** -8 + 2 ** -15))
+    q64, q = bf(rng.standard_normal((1, 1, H, DIM)))
+    for idx in (None, rng.choice(L - 1, 64, replace=False).astype(np.int32)[None, None]):
+        out, lse = X.tree_mla(q.cuda(), cache, dev(table), dev(np.array([L], np.int32)), SCALE, max_len=L,
+                              indices=None if idx is None else dev(idx))
+        assert X.status() == (0, 0)
+        from tests.paged_helpers import UB, tree_row
+        pos = list(range(L)) if idx is None else list(idx[0, 0]) + [L - 1]
+        o, ls, bound, lerr = tree_row(q64[0, 0], got[pos], SCALE)
+        assert np.all(np.abs(out[0, 0].double().cpu().numpy() - o) <= bound + UB * np.abs(o) * (1 + UB) + 1e-30)
+        assert np.all(np.abs(lse[0, 0].double().cpu().numpy() - ls) <= lerr)
+
+
+@pytest.mark.parametrize("H,ctx", [(16, 3000), (30, 3000), (60, 3000), (128, 3000)])
+def test_a_wait_that_runs_out_ends_the_call(H, ctx):
+    """The second tile's scores wait for a barrier that nothing signals, for 2 ms:
+    every warp of every CTA gives up, the call returns with the error word set and
+    the next call is right."""
+    from sparse_attention_token_idx_b200 import binding as X
+    rng = np.random.default_rng(14)
+    paged = Paged(rng, [ctx, 700, 5], 64).fill(rng)
+    q64, q = bf(rng.standard_normal((3, 1, H, DIM)))
+    args = (q.cuda(), paged.cache_dev(), paged.table_dev(), dev(np.array(paged.lens, np.int32)), SCALE)
+    X.tree_mla(*args, max_len=ctx)
+    assert X.status() == (0, 0)
+    X.debug_set(1, 2_000_000)
+    try:
+        X.tree_mla(*args, max_len=ctx)
+        assert X.status() == (-7, X.DEV_ERR_TIMEOUT)
+    finally:
+        X.debug_set(0, 0)
+    out, lse = X.tree_mla(*args, max_len=ctx)
+    assert X.status() == (0, 0)
+    check_tree(out, lse, q64, paged, [1, 1, 1], SCALE)
