@@ -4,6 +4,8 @@ weights, then score every query row against the cache and select its top-k.
 
 ``Indexer`` owns the cache buffers (kept between calls) and the per-call
 scratch tensors; every step runs in libidx.so through ``binding``.
+``LatentCache`` owns the paged cache of the attention that follows: it hands out
+pages, appends the new tokens' rows and attends to them.
 """
 from __future__ import annotations
 
@@ -104,6 +106,22 @@ class Indexer:
         return self.step_front(q_proj, w_raw, k_proj, rope_cos, rope_sin, ln_gain, ln_bias, positions, lengths,
                                causal=causal, max_len=max_len, ln_eps=ln_eps, out=out, stream=stream)
 
+    def select(self, q, w_raw, lengths, *, max_len: int, out=None, stream=None):
+        """Top-k positions [B, n, k] int32 of n query rows per sequence over its first
+        lengths[b] cached keys (n ≤ lengths[b] ≤ max_len), nothing appended: what
+        the rows of a drafted tree attend to in their context (every row sees all of
+        it; the drafts themselves are LatentCache.attend's).  q [B, n, 64, 128] bf16,
+        w_raw [B, n, 64] fp32."""
+        B, n = q.shape[0], q.shape[1]
+        q_fp8 = self._buf("q_fp8", tuple(q.shape), torch.uint8)
+        w = self._buf("w", tuple(w_raw.shape), torch.float32)
+        X.quant_queries(q, w_raw, self.fmt, q_fp8, w, stream=stream)
+        out = out if out is not None else self._buf("idx", (B, n, self.k), torch.int32)
+        ws_bytes = X.workspace_size(B, n, max_len, self.k)
+        ws = self._buf("ws", (ws_bytes,), torch.uint8) if ws_bytes else None
+        return X.score_topk_ex(q_fp8, w, self.k_cache, self.k_scale_cache, lengths, False, self.k, max_len, out=out,
+                               ws=ws, stream=stream)
+
     def projections(self):
         """(q_proj, k_proj, w_raw) of the last step_hidden."""
         return self._bufs["q_proj"], self._bufs["k_proj"], self._bufs["w_raw"]
@@ -123,6 +141,93 @@ class Indexer:
         with torch.cuda.graph(g):
             self.step(k_new, q, w_raw, positions, lengths, causal=causal, max_len=max_len, out=out)
         return g, out
+
+
+class LatentCache:
+    """The paged cache of latent rows (576 bf16 each) of B sequences, and the two
+    steps that use it: append (norm, rotation, write) and attend (the drafted rows
+    of every sequence over their contexts).
+
+    Pages belong to sequences: reserve(b, length) gives sequence b as many as
+    `length` rows need, release(b) takes them back; share(b, of, length) lets b
+    read the whole pages of another sequence's prefix.  The page table is kept on
+    the host and uploaded by the next call after it has changed, on that call's
+    stream; not inside a capture, where the table must be up to date (table())."""
+
+    def __init__(self, B: int, num_pages: int, page_size: int, max_len: int, device="cuda"):
+        if min(B, num_pages, page_size, max_len) < 1:
+            raise ValueError("LatentCache: sizes must be positive")
+        self.B, self.num_pages, self.page_size, self.max_len = B, num_pages, page_size, max_len
+        self.device = torch.device(device)
+        self.max_pages = -(-max_len // page_size)
+        self.cache = torch.zeros((num_pages, page_size, X.LATENT + X.ROTARY), dtype=torch.bfloat16, device=self.device)
+        self.page_table = torch.full((B, self.max_pages), -1, dtype=torch.int32, device=self.device)
+        self._table = torch.full((B, self.max_pages), -1, dtype=torch.int32)
+        self._pages = [[] for _ in range(B)]
+        self._users = [0] * num_pages
+        self._free = list(range(num_pages - 1, -1, -1))
+        self._stale = False
+
+    def _give(self, b: int, page: int):
+        self._users[page] += 1
+        self._table[b, len(self._pages[b])] = page
+        self._pages[b].append(page)
+        self._stale = True
+
+    def reserve(self, b: int, length: int):
+        """Make sure that sequence b has pages for `length` rows."""
+        if not 0 <= length <= self.max_len:
+            raise ValueError(f"LatentCache: length {length} outside [0, {self.max_len}]")
+        more = -(-length // self.page_size) - len(self._pages[b])
+        if more > len(self._free):
+            raise X.IdxError(f"LatentCache: {more} pages wanted, {len(self._free)} free")
+        for _ in range(more):
+            self._give(b, self._free.pop())
+
+    def release(self, b: int):
+        """Take sequence b's pages back (a page goes when its last sequence does)."""
+        for page in self._pages[b]:
+            self._users[page] -= 1
+            if self._users[page] == 0:
+                self._free.append(page)
+        self._pages[b] = []
+        self._table[b] = -1
+        self._stale = True
+
+    def share(self, b: int, of: int, length: int) -> int:
+        """Give sequence b (which has no pages) the whole pages of sequence `of`'s
+        first `length` rows, to read; returns how many rows those are.  Rows are
+        appended behind them only."""
+        if self._pages[b]:
+            raise ValueError("LatentCache: share() before the sequence has pages")
+        whole = min(length // self.page_size, len(self._pages[of]))
+        for page in self._pages[of][:whole]:
+            self._give(b, page)
+        return whole * self.page_size
+
+    def table(self, stream=None):
+        """The device page table, brought up to date (on `stream`, or the current one)."""
+        if self._stale:
+            with torch.cuda.stream(stream):
+                if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+                    raise X.IdxError("LatentCache: the page table changed; call table() before the capture")
+                self.page_table.copy_(self._table)
+            self._stale = False
+        return self.page_table
+
+    def append(self, kv_proj, gain, eps, rope_cos, rope_sin, positions, *, interleaved=True, counts=None, q_pe=None,
+               q_out=None, stream=None):
+        """New tokens' rows at slots positions[b] … (see binding.latent_append)."""
+        return X.latent_append(kv_proj, gain, eps, rope_cos, rope_sin, positions, self.table(stream), self.cache,
+                               interleaved=interleaved, counts=counts, q_pe=q_pe, q_out=q_out, stream=stream)
+
+    def attend(self, q, lengths, softmax_scale, *, max_len=None, counts=None, tree_mask=None, indices=None, out=None,
+               lse=None, stream=None):
+        """Latent attention of each sequence's last rows (see binding.tree_mla), over
+        the whole context or over an indexer's selection of it (Indexer.select)."""
+        return X.tree_mla(q, self.cache, self.table(stream), lengths, softmax_scale,
+                          max_len=self.max_len if max_len is None else max_len, counts=counts, tree_mask=tree_mask,
+                          indices=indices, out=out, lse=lse, stream=stream)
 
 
 class HostPipeline:

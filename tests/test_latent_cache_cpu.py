@@ -1,0 +1,40 @@
+"""Page bookkeeping of LatentCache (host logic, on CPU tensors)."""
+import pytest
+import torch
+
+from sparse_attention_token_idx_b200 import binding as X
+from sparse_attention_token_idx_b200.pipeline import LatentCache
+
+
+def test_pages_are_reserved_released_and_shared():
+    c = LatentCache(3, 6, 16, 64, device="cpu")
+    assert c.max_pages == 4 and (c.table() == -1).all()
+    c.reserve(0, 33)                                             # three pages
+    c.reserve(0, 20)                                             # nothing more
+    t = c.table()
+    held = t[0, :3].tolist()
+    assert len(set(held)) == 3 and t[0, 3] == -1 and (t[1:] == -1).all()
+    assert c.share(1, 0, 40) == 32                               # whole pages only
+    assert c.table()[1, :2].tolist() == held[:2]
+    c.reserve(1, 48)
+    assert c.table()[1, 2].item() not in held
+    c.release(0)                                                 # its third page is free again, the shared ones are not
+    c.reserve(2, 48)
+    assert not set(c.table()[2, :3].tolist()) & set(c.table()[1, :3].tolist())
+    with pytest.raises(X.IdxError):
+        c.reserve(0, 1)                                          # none left
+    c.release(1)
+    c.release(2)
+    assert sorted(c._free) == list(range(6)) and c._users == [0] * 6
+
+
+def test_refusals():
+    with pytest.raises(ValueError):
+        LatentCache(1, 0, 16, 64, device="cpu")
+    c = LatentCache(2, 4, 16, 32, device="cpu")
+    with pytest.raises(ValueError):
+        c.reserve(0, 33)
+    c.reserve(0, 16)
+    with pytest.raises(ValueError):
+        c.share(0, 1, 16)
+    assert c.page_table.dtype == torch.int32
