@@ -26,7 +26,10 @@
 //   warps 3-6  copy the tiles' rows by cp.async, 16 bytes a lane; a key that no row
 //              sees arrives as zeros, never as what memory holds.  (TMA delivers these
 //              1 152-byte rows at 25 B/clk per SM in boxes and 9 – 20 gathered, cp.async
-//              at 34 – 70 with 4 – 16 warps from L2 and 26 from HBM, its limit.)
+//              at 34 – 70 with 4 – 16 warps from L2 and 26 from HBM, its limit.  Asking
+//              for selected rows in L2 ahead of the copies was measured, up to four tiles
+//              ahead, by lines and by rows: 5 – 10% less time where HBM is idle (16 x 7
+//              tokens), up to 17% more where it is not (128 tokens with rows of their own).)
 //   warps 7 …  softmax: thread ↔ (key, part of the rows).  Scores are compared with
 //              a running reference maximum per row as it is; only where one passes it
 //              by 2^8 (a piece's first tile always) the column maxima are reduced, by a
@@ -55,8 +58,7 @@ struct Cfg {
   static constexpr int kSoftWarps = N == 64 ? 16 : 8;
   static constexpr int kParts = kSoftWarps / 4;             // row parts, each of four warps (128 keys)
   static constexpr int kNC = N / kParts;                    // rows per softmax thread
-  static constexpr int kPrefetchWarp = kFirstSoft + kSoftWarps;
-  static constexpr int kThreads = (kPrefetchWarp + 1) * 32;
+  static constexpr int kThreads = (kFirstSoft + kSoftWarps) * 32;
   static constexpr int kPairs = N == 16 ? 5 : 4;            // latent buffers
   static constexpr int kRopes = N == 32 ? 2 : 1;            // rotary-chunk buffers
   static constexpr bool kAliasP = N == 64;                  // P takes the rotary chunk's place after the scores
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc<N>& ms = *reinterpret_cast<Misc<N>*>(smem + C::kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
+  const int team = blockIdx.x / p.halves;
   const Waits waits{p.budget_ns, &ms.abort_flag, p.err};
 
   if (threadIdx.x == 0) {
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     mbar_init(&ms.o_free, C::kSoftWarps);
     for (int i = 0; i < 2; ++i) mbar_init(&ms.drain_bar[i], 1);
     for (int i = 0; i < C::kParts; ++i) ms.left_at[i] = 0;
-    ms.init(p.B, kCopyWarps + C::kSoftWarps + (p.indices ? 1 : 0), C::kSoftWarps + 2);
+    ms.init(p.B, kCopyWarps + C::kSoftWarps, C::kSoftWarps + 2);
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
   }
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp == 0) {
-    plan<N, kTile>(p, ms, share, rank, waits, [&](int row0) {
+    plan<N, kTile>(p, ms, share, waits, [&](int row0) {
       mbar_arrive_expect_tx(&ms.q_full, 9 * N * 128);
       for (int c = 0; c < 9; ++c)
         tma_box(smem_base + C::kOffQ + c * N * 128, &tmap_q, smem_u32(&ms.q_full), c * 64, row0);
@@ -167,9 +169,27 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         // Sᵀ = K · qᵀ, once the softmax has read the last S, chunk by chunk as they land
         if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
         if (p.fault && tiles == 1 && !(ok = waits(&ms.never, 0))) break;
-        for (int u = 0; u < 4; ++u) {
-          if (!(ok = waits(&ms.pair_full[slot], lap & 1))) break;
+        // (the rotary chunk first where its place is free since the last scores, so that
+        // less follows the last copy; last where P held it)
+        const int rs = tiles % C::kRopes;
+        auto rope_scores = [&] {
+          if (!(ok = waits(&ms.rope_full[rs], (tiles / C::kRopes) & 1))) return;
           fence_proxy_async_smem();                        // the copies wrote through the generic proxy
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t a = k_desc + static_cast<uint64_t>((C::kOffRope + rs * kChunk) >> 4);
+            const uint64_t q = q_desc + static_cast<uint64_t>(8 * N * 128 >> 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_f16(d_s, a + i * 2, q + i * 2, id_s, (C::kAliasP || i > 0) ? 1u : 0u);
+            if (!C::kAliasP) mma_commit(&ms.rope_empty[rs]);
+          }
+          issued = true;
+          __syncwarp();
+        };
+        if (!C::kAliasP) rope_scores();
+        for (int u = 0; u < 4 && ok; ++u) {
+          if (!(ok = waits(&ms.pair_full[slot], lap & 1))) break;
+          fence_proxy_async_smem();
           tc_fence_after();
           if (elect_one()) {
             const uint64_t a = k_desc + static_cast<uint64_t>(slot * (kPair >> 4));
@@ -177,24 +197,17 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               mma_f16(d_s, a + static_cast<uint64_t>((i >> 2) * (kChunk >> 4) + (i & 3) * 2),
-                      q + static_cast<uint64_t>((i >> 2) * (N * 128 >> 4) + (i & 3) * 2), id_s, (u > 0 || i > 0) ? 1u : 0u);
+                      q + static_cast<uint64_t>((i >> 2) * (N * 128 >> 4) + (i & 3) * 2), id_s,
+                      (!C::kAliasP || u > 0 || i > 0) ? 1u : 0u);
           }
           issued = true;
           __syncwarp();
           if (++slot == C::kPairs) slot = 0, ++lap;
         }
+        if (ok && C::kAliasP) rope_scores();
         if (!ok) break;
-        const int rs = tiles % C::kRopes;
-        if (!(ok = waits(&ms.rope_full[rs], (tiles / C::kRopes) & 1))) break;
-        fence_proxy_async_smem();
-        tc_fence_after();
         if (elect_one()) {
-          const uint64_t a = k_desc + static_cast<uint64_t>((C::kOffRope + rs * kChunk) >> 4);
-          const uint64_t q = q_desc + static_cast<uint64_t>(8 * N * 128 >> 4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mma_f16(d_s, a + i * 2, q + i * 2, id_s, 1u);
           mma_commit(&ms.s_full);
-          if (!C::kAliasP) mma_commit(&ms.rope_empty[rs]);
           if (c == n - 1) mma_commit(&ms.q_empty);
         }
         __syncwarp();
@@ -286,7 +299,20 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       for (int j = 0; j < kRopeRuns; ++j) rope_row[j] = ms.row[par][key1 + kRopeStep * j];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.tile_read[par]);
-      for (int u = 0; u < 4; ++u) {
+      auto copy_rope = [&] {
+        const int sl = ropes % C::kRopes;
+        if (ropes >= C::kRopes && !(ok = waits.nap(&ms.rope_empty[sl], (ropes / C::kRopes - 1) & 1))) return;
+        const uint32_t to = to_rope + sl * kChunk;
+        const uint8_t* src = from + 2 * kLat + (lane & 7) * 16;
+#pragma unroll
+        for (int j = 0; j < kRopeRuns; ++j)
+          cp_async16(to + j * (kRopeStep * 128), src + static_cast<int64_t>(max(rope_row[j], 0)) * (2 * kRow),
+                     rope_row[j] >= 0 ? 16 : 0);
+        cp_async_arrive(&ms.rope_full[sl]);
+        ++ropes;
+      };
+      if (!C::kAliasP) copy_rope();
+      for (int u = 0; u < 4 && ok; ++u) {
         const int sl = pairs % C::kPairs;
         if (pairs >= C::kPairs && !(ok = waits.nap(&ms.pair_empty[sl], (pairs / C::kPairs - 1) & 1))) break;
         const uint32_t to = to_pair + sl * kPair;
@@ -298,25 +324,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         ++pairs;
       }
       if (!ok) break;
-      const int sl = ropes % C::kRopes;
-      if (ropes >= C::kRopes && !(ok = waits.nap(&ms.rope_empty[sl], (ropes / C::kRopes - 1) & 1))) break;
-      const uint32_t to = to_rope + sl * kChunk;
-      const uint8_t* src = from + 2 * kLat + (lane & 7) * 16;
-#pragma unroll
-      for (int j = 0; j < kRopeRuns; ++j)
-        cp_async16(to + j * (kRopeStep * 128), src + static_cast<int64_t>(max(rope_row[j], 0)) * (2 * kRow),
-                   rope_row[j] >= 0 ? 16 : 0);
-      cp_async_arrive(&ms.rope_full[sl]);
-      ++ropes;
+      if (C::kAliasP) copy_rope();
       ++tiles;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");       // they have landed before the memory goes
-  } else if (warp == C::kPrefetchWarp) {
-    // ================================================================ prefetch
-    // selections only: their rows are scattered, and a tile and a quarter of buffers
-    // does not cover the latency of HBM.  A dense walk keeps HBM busy by itself, and
-    // asking ahead takes from it: 235 us with, 225 without, at 16 x 131 000 positions
-    if (p.indices) prefetch_tiles<kTile>(p, ms, waits, 0, 1);
   } else {
     // ================================================================ softmax
     constexpr int kColShift = NC == 16 ? 1 : 2;

@@ -86,6 +86,9 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
+__device__ __forceinline__ void prefetch_l2_row(const void* src) {   // a cache row, 16-byte aligned
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "n"(2 * kRow) : "memory");
+}
 // 32 bytes of one thread: a whole sector (32-byte aligned)
 __device__ __forceinline__ void st_global32(void* dst, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
@@ -392,8 +395,7 @@ __device__ __forceinline__ Share find_share(const TreeParams& p, State& ms, int 
 // rows see of the drafts) and each tile (cache rows of its keys), and has the
 // piece's queries loaded: load_q(row0) issues them on ms.q_full.
 template <int M, int KT, class State, class LoadQ>
-__device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share& sh, int rank, const Waits& waits,
-                                     LoadQ load_q) {
+__device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share& sh, const Waits& waits, LoadQ load_q) {
   constexpr int E = KT / 32;                  // keys per lane
   const int lane = threadIdx.x & 31;
   bool ok = true;
@@ -544,24 +546,6 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
   }
   if (!p.whole && lane == 0) p.cuts[blockIdx.x] = cut;
   if (pieces) waits.drain(&ms.q_full, (pieces - 1) & 1);   // landed before the memory goes
-}
-
-// A warp that asks for the tiles' 128-byte lines in L2, up to kAhead tiles before
-// their copies: its `part` of `parts`.
-template <int KT, class State>
-__device__ __forceinline__ void prefetch_tiles(const TreeParams& p, State& ms, const Waits& waits, int part, int parts) {
-  const int lane = threadIdx.x & 31;
-  const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
-  for (int tiles = 0;; ++tiles) {
-    const int at = tiles % kAhead;
-    if (!waits.nap(&ms.tile_full[at], (tiles / kAhead) & 1) || ms.last[at]) break;
-    for (int i = part * 32 + lane; i < KT * 9; i += 32 * parts) {
-      const int r = ms.row[at][i / 9];
-      if (r >= 0) prefetch_l2(from + static_cast<int64_t>(r) * (2 * kRow) + i % 9 * 128);
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ms.tile_read[at]);
-  }
 }
 
 __device__ __forceinline__ float lse_of(float m, float z) {    // m in log2 units

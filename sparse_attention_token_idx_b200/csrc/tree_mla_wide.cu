@@ -80,8 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   WideState& ms = *reinterpret_cast<WideState*>(smem + kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
-  const int half = rank;
+  const int team = blockIdx.x / p.halves, half = blockIdx.x % p.halves;
   const Waits waits{p.budget_ns, &ms.abort_flag, p.err};
 
   if (threadIdx.x == 0) {
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp == 0) {
-    plan<kRows, kKeys>(p, ms, share, rank, waits, [&](int row0) {
+    plan<kRows, kKeys>(p, ms, share, waits, [&](int row0) {
       mbar_arrive_expect_tx(&ms.q_full, 3 * kQChunk);
       for (int c = 0; c < 3; ++c)
         tma_box(smem_base + kOffQ + c * kQChunk, &tmap_q, smem_u32(&ms.q_full), feature_chunk(kQTmem + c, half) * 64,
@@ -282,7 +281,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");       // they have landed before the memory goes
   } else if (warp == kPrefetchWarp) {
     // ================================================================ prefetch
-    prefetch_tiles<kKeys>(p, ms, waits, half, 2);
+    // this CTA's half of the rows, one bulk request each (128 x 2 048 selected positions
+    // of 16 384, 128 heads: 139 us, 149 without the warp; 128 x 8 drafted heads over
+    // 32 x 8 192: 332 and 345)
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
+    for (int tiles = 0;; ++tiles) {
+      const int at = tiles % kAhead;
+      if (!waits.nap(&ms.tile_full[at], (tiles / kAhead) & 1) || ms.last[at]) break;
+      const int r = ms.row[at][half * 32 + lane];
+      if (r >= 0) prefetch_l2_row(from + static_cast<int64_t>(r) * (2 * kRow));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.tile_read[at]);
+    }
   } else {
     // ================================================================ softmax
     const int sw = warp - kFirstSoft, quad = warp & 3, part = sw >> 2;
