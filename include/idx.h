@@ -425,7 +425,8 @@ enum idx_out_dtype { IDX_OUT_F32 = 0, IDX_OUT_BF16 = 1 };
  *            bytes, 32-byte aligned (may be NULL where that is 0).  It holds
  *            partial results inside the call: calls (or captured graphs) that may
  *            run at the same time need one each.
- * q, cache: 16-byte aligned; out, ws 32; tree_mask 8.  Scores and sums in fp32.
+ * q, cache: 16-byte aligned; out, ws 32; tree_mask 8.  Scores and sums in fp32;
+ * softmax_scale may be negative or 0; |softmax_scale| · log2 e must be finite in fp32.
  * Errors: IDX_ERR_SHAPE, IDX_ERR_NULL, IDX_ERR_ALIGN, IDX_ERR_FMT (out_dtype),
  * IDX_ERR_SCRATCH.  counts[b] outside [0, n], lengths[b] < counts[b] or
  * lengths[b] > max_len raise IDX_DEV_ERR_LENGTH and leave the sequence's outputs as

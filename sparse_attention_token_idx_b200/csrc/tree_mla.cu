@@ -663,7 +663,7 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
   constexpr int64_t kMaxRows = 0x7FFFFFFF;
   if (out_dtype != IDX_OUT_F32 && out_dtype != IDX_OUT_BF16) return IDX_ERR_FMT;
   if (B < 0 || n < 0 || n > IDX_MAX_DRAFTS || H <= 0 || k < 0 || k > kMaxRows - 2 * kTile - IDX_MAX_DRAFTS ||
-      !std::isfinite(softmax_scale))
+      !std::isfinite(softmax_scale * kLog2e))
     return IDX_ERR_SHAPE;
   if (B == 0 || n == 0) return IDX_OK;
   if (max_pages <= 0 || num_pages <= 0 || page_size <= 0 || static_cast<int64_t>(num_pages) * page_size > kMaxRows ||

@@ -60,6 +60,12 @@ def test_tree_host_checks(kw, code):
     assert _tree(binding.load(), **kw) == code
 
 
+@pytest.mark.parametrize("scale,code", [(2.36e38, SHAPE), (-3.0e38, SHAPE), (2.3e38, NULL)])
+def test_tree_refuses_a_scale_that_overflows_in_log2_units(scale, code):
+    from sparse_attention_token_idx_b200 import binding
+    assert _tree(binding.load(), scale=scale, q=None) == code      # (q = NULL: the next check)
+
+
 def test_wrappers_reject_shapes_and_types_before_the_library():
     from sparse_attention_token_idx_b200 import binding as X
     bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
