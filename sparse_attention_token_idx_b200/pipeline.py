@@ -152,7 +152,9 @@ class LatentCache:
     `length` rows need, release(b) takes them back; share(b, of, length) lets b
     read the whole pages of another sequence's prefix.  The page table is kept on
     the host and uploaded by the next call after it has changed, on that call's
-    stream; not inside a capture, where the table must be up to date (table())."""
+    stream; not inside a capture, where the table must be up to date (table()).
+    Calls on several streams are ordered by their user, as with any tensor: an
+    upload must not overtake a call that still reads pages released since."""
 
     def __init__(self, B: int, num_pages: int, page_size: int, max_len: int, device="cuda"):
         if min(B, num_pages, page_size, max_len) < 1:
@@ -168,6 +170,11 @@ class LatentCache:
         self._free = list(range(num_pages - 1, -1, -1))
         self._stale = False
 
+    def _held(self, b: int) -> list:
+        if not 0 <= b < self.B:
+            raise ValueError(f"LatentCache: sequence {b} outside [0, {self.B})")
+        return self._pages[b]
+
     def _give(self, b: int, page: int):
         self._users[page] += 1
         self._table[b, len(self._pages[b])] = page
@@ -178,7 +185,7 @@ class LatentCache:
         """Make sure that sequence b has pages for `length` rows."""
         if not 0 <= length <= self.max_len:
             raise ValueError(f"LatentCache: length {length} outside [0, {self.max_len}]")
-        more = -(-length // self.page_size) - len(self._pages[b])
+        more = -(-length // self.page_size) - len(self._held(b))
         if more > len(self._free):
             raise X.IdxError(f"LatentCache: {more} pages wanted, {len(self._free)} free")
         for _ in range(more):
@@ -186,7 +193,7 @@ class LatentCache:
 
     def release(self, b: int):
         """Take sequence b's pages back (a page goes when its last sequence does)."""
-        for page in self._pages[b]:
+        for page in self._held(b):
             self._users[page] -= 1
             if self._users[page] == 0:
                 self._free.append(page)
@@ -198,9 +205,11 @@ class LatentCache:
         """Give sequence b (which has no pages) the whole pages of sequence `of`'s
         first `length` rows, to read; returns how many rows those are.  Rows are
         appended behind them only."""
-        if self._pages[b]:
+        if self._held(b):
             raise ValueError("LatentCache: share() before the sequence has pages")
-        whole = min(length // self.page_size, len(self._pages[of]))
+        if length < 0:
+            raise ValueError(f"LatentCache: length {length} is negative")
+        whole = min(length // self.page_size, len(self._held(of)))
         for page in self._pages[of][:whole]:
             self._give(b, page)
         return whole * self.page_size

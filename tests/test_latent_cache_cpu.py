@@ -28,6 +28,18 @@ def test_pages_are_reserved_released_and_shared():
     assert sorted(c._free) == list(range(6)) and c._users == [0] * 6
 
 
+def test_sequences_and_lengths_out_of_range_are_refused():
+    c = LatentCache(2, 6, 16, 64, device="cpu")
+    c.reserve(1, 48)
+    for call in (lambda: c.share(0, 1, -1), lambda: c.share(0, 2, 16), lambda: c.share(-1, 0, 16),
+                 lambda: c.reserve(-1, 16), lambda: c.reserve(2, 16), lambda: c.reserve(0, -1),
+                 lambda: c.release(-1), lambda: c.release(2)):
+        with pytest.raises(ValueError):
+            call()
+    assert c.share(0, 1, 0) == 0
+    assert (c.table()[0] == -1).all() and (c.table()[1, :3] >= 0).all() and len(c._free) == 3
+
+
 def test_refusals():
     with pytest.raises(ValueError):
         LatentCache(1, 0, 16, 64, device="cpu")
