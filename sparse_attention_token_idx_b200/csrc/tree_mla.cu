@@ -30,6 +30,9 @@
 //              for selected rows in L2 ahead of the copies was measured, up to four tiles
 //              ahead, by lines and by rows: 5 – 10% less time where HBM is idle (16 x 7
 //              tokens), up to 17% more where it is not (128 tokens with rows of their own).)
+//              A key set's rows are read by this CTA alone, so they are the first to
+//              leave L2: 128 tokens of 2 048 rows 84 -> 74 us, 16 x 131 000 positions
+//              242 -> 239; in the wide kernel, where two CTAs read them, 139 -> 150;
 //   warps 7 …  softmax: thread ↔ (key, part of the rows).  Scores are compared with
 //              a running reference maximum per row as it is; only where one passes it
 //              by 2^8 (a piece's first tile always) the column maxima are reduced, by a
@@ -287,6 +290,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     const int key1 = 4 * w + (lane >> 3);
     const uint32_t to_rope = smem_base + C::kOffRope + key1 * 128 + (((lane & 7) ^ (key1 & 7)) << 4);
     const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
+    const uint64_t once = once_policy();
     int pairs = 0, ropes = 0, tiles = 0;
     bool ok = true;
     while (ok) {
@@ -306,8 +310,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         const uint8_t* src = from + 2 * kLat + (lane & 7) * 16;
 #pragma unroll
         for (int j = 0; j < kRopeRuns; ++j)
-          cp_async16(to + j * (kRopeStep * 128), src + static_cast<int64_t>(max(rope_row[j], 0)) * (2 * kRow),
-                     rope_row[j] >= 0 ? 16 : 0);
+          cp_async16_once(to + j * (kRopeStep * 128), src + static_cast<int64_t>(max(rope_row[j], 0)) * (2 * kRow),
+                     rope_row[j] >= 0 ? 16 : 0, once);
         cp_async_arrive(&ms.rope_full[sl]);
         ++ropes;
       };
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         const uint8_t* src = from + u * 256 + piece * 16;
 #pragma unroll
         for (int j = 0; j < kRuns; ++j)
-          cp_async16(to + j * (kStep * 128), src + static_cast<int64_t>(max(row[j], 0)) * (2 * kRow), row[j] >= 0 ? 16 : 0);
+          cp_async16_once(to + j * (kStep * 128), src + static_cast<int64_t>(max(row[j], 0)) * (2 * kRow), row[j] >= 0 ? 16 : 0, once);
         cp_async_arrive(&ms.pair_full[sl]);
         ++pairs;
       }
@@ -540,12 +544,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Joins the pieces of the items that shares cut: CTA (x, y) takes every kJoinY-th
+// Joins the pieces of the items that shares cut (its share of a call: 2 us for the
+// launch, 5 for the 38 MB of 73 cut items of 128 rows): CTA (x, y) takes every kJoinY-th
 // run of outputs of the item that begins in CTA x's share and goes on in the next
 // teams'.  A thread ↔ eight output features of a row, walking the pieces with a
 // running maximum; many pieces (one long sequence) are split over four threads,
 // whose results are added in a fixed order.  Reads what the pieces wrote, from L2.
-constexpr int kJoinThreads = 256, kJoinY = 8;
+constexpr int kJoinThreads = 128, kJoinY = 16;
 struct Joined {
   float o[8], top, z;
 };
@@ -577,13 +582,21 @@ __global__ void __launch_bounds__(kJoinThreads) tree_mla_join_kernel(const TreeP
     const int at = p.halves == 1 ? c * D + d * 8 : (d * p.M + c) * 8;
     const int at_m = p.M * D + c, at_z = at_m + p.M;
     Joined a{{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, -INFINITY, 0.f};
-#pragma unroll 4
-    for (int i = group; i <= cut.pieces; i += split) {
-      const float* s = i == 0 ? first : next + i * stride;   // piece 0: this team's slot 1; then the next teams' slot 0
-      const float m = s[at_m], z = s[at_z];
-      const float4 x0 = *reinterpret_cast<const float4*>(s + at), x1 = *reinterpret_cast<const float4*>(s + at + 4);
-      const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-      join_add(a, m, z, x);
+    // two pieces at a time (an item has at least two): their loads are in flight together
+    for (int i = group; i <= cut.pieces; i += 2 * split) {
+      float m[2], z[2];
+      float4 x[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int piece = min(i + h * split, cut.pieces);
+        const float* s = piece == 0 ? first : next + piece * stride;   // 0: this team's slot 1; then the next teams' slot 0
+        m[h] = s[at_m];
+        z[h] = s[at_z];
+        x[h][0] = *reinterpret_cast<const float4*>(s + at);
+        x[h][1] = *reinterpret_cast<const float4*>(s + at + 4);
+      }
+      join_add(a, m[0], z[0], reinterpret_cast<const float*>(x[0]));
+      if (i + split <= cut.pieces) join_add(a, m[1], z[1], reinterpret_cast<const float*>(x[1]));
     }
     if (split > 1) {
       part[threadIdx.x] = a;
