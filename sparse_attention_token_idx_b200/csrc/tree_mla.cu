@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       for (int c = 0; c < n && ok; ++c) {
         // Sᵀ = K · qᵀ, once the softmax has read the last S, chunk by chunk as they land
         if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
-        if (p.fault && tiles == 1 && !(ok = waits(&ms.never, 0))) break;
+        if (p.fault && c == n - 1 && !(ok = waits(&ms.never, 0))) break;
         // (the rotary chunk first where its place is free since the last scores, so that
         // less follows the last copy; last where P held it)
         const int rs = tiles % C::kRopes;
@@ -544,13 +544,16 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Joins the pieces of the items that shares cut (its share of a call: 2 us for the
-// launch, 5 for the 38 MB of 73 cut items of 128 rows): CTA (x, y) takes every kJoinY-th
-// run of outputs of the item that begins in CTA x's share and goes on in the next
-// teams'.  A thread ↔ eight output features of a row, walking the pieces with a
-// running maximum; many pieces (one long sequence) are split over four threads,
-// whose results are added in a fixed order.  Reads what the pieces wrote, from L2.
-constexpr int kJoinThreads = 128, kJoinY = 16;
+// Joins the pieces of the items that shares cut.  A unit is 32 runs of eight output
+// features of such an item, a lane each, walking the pieces with a running maximum.
+// CTA (x, y) takes every kJoinY-th eight units, a warp each, of the item that begins
+// in CTA x's share, where it has few pieces.  Items of kJoinSplit pieces and more
+// (one long sequence over all SMs is one item) are dealt to all CTAs: one unit at a
+// time, whose pieces the CTA's eight warps share; their results are added in a
+// fixed order (64 heads over one sequence of 131 072: 69 us a call, 147 when CTA x
+// alone took its item).  Reads what the pieces wrote, from L2 as far as it is
+// still there; two pieces of each of 128 items of 128 rows, 38 MB: 6 us.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinY = 8, kJoinSplit = 8;
 struct Joined {
   float o[8], top, z;
 };
@@ -562,87 +565,145 @@ __device__ __forceinline__ void join_add(Joined& a, float m, float z, const floa
   a.z = a.z * keep + w * z;
   a.top = up;
 }
+// pieces first, first + step … ≤ last of a run, K of them in flight at a time
+struct PieceRun {
+  const float *head, *next;                   // piece 0; piece i > 0 lies at next + i · stride
+  int64_t stride;
+  int at, at_m, at_z;
+};
+template <int K>
+__device__ __forceinline__ Joined join_pieces(const PieceRun& r, int first, int step, int last) {
+  Joined a{{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, -INFINITY, 0.f};
+  for (int i = first; i <= last; i += K * step) {
+    float m[K], z[K];
+    float4 x[K][2];
+#pragma unroll
+    for (int h = 0; h < K; ++h) {
+      const int piece = min(i + h * step, last);
+      const float* s = piece == 0 ? r.head : r.next + piece * r.stride;
+      m[h] = s[r.at_m];
+      z[h] = s[r.at_z];
+      x[h][0] = *reinterpret_cast<const float4*>(s + r.at);
+      x[h][1] = *reinterpret_cast<const float4*>(s + r.at + 4);
+    }
+#pragma unroll
+    for (int h = 0; h < K; ++h)
+      if (i + h * step <= last) join_add(a, m[h], z[h], reinterpret_cast<const float*>(x[h]));
+  }
+  return a;
+}
+struct Unit {                                 // a lane's run of an item
+  int row, feature, valid;
+  PieceRun run;
+};
+__device__ __forceinline__ Unit join_unit(const TreeParams& p, const Cut& cut, int cta, int unit, int lane) {
+  const int D = kLat / p.halves, D8 = D / 8, count = cut.rows * D8;   // output features per slot row
+  // neighbours in memory are neighbours in the warp: features of a row, or rows
+  const int e = min(unit * 32 + lane, count - 1);
+  const int c = p.halves == 1 ? e / D8 : e % cut.rows, d = p.halves == 1 ? e % D8 : e / cut.rows;
+  Unit u;
+  u.row = c;
+  u.feature = cta % p.halves * D + d * 8;
+  u.valid = unit * 32 + lane < count;
+  u.run.head = part_slot(p, cta, 1);           // it begins in this share; the next teams' slots 0 go on
+  u.run.next = part_slot(p, cta, 0);
+  u.run.stride = static_cast<int64_t>(p.halves) * 2 * p.M * (D + 2);
+  u.run.at = p.halves == 1 ? c * D + d * 8 : (d * p.M + c) * 8;
+  u.run.at_m = p.M * D + c;
+  u.run.at_z = u.run.at_m + p.M;
+  return u;
+}
+__device__ __forceinline__ void join_store(const TreeParams& p, const Cut& cut, const Unit& u, Joined& a) {
+  if (!u.valid) return;
+  const float inv = a.z == 0.f ? 0.f : 1.f / a.z;
+  const int64_t to = (cut.row0 + u.row) * kLat + u.feature;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a.o[i] *= inv;
+  if (p.out_bf16) {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to) =
+        make_uint4(bf_pack(a.o[0], a.o[1]), bf_pack(a.o[2], a.o[3]), bf_pack(a.o[4], a.o[5]), bf_pack(a.o[6], a.o[7]));
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + to);
+    dst[0] = make_float4(a.o[0], a.o[1], a.o[2], a.o[3]);
+    dst[1] = make_float4(a.o[4], a.o[5], a.o[6], a.o[7]);
+  }
+  if (p.lse && u.feature == 0) p.lse[cut.row0 + u.row] = lse_of(a.top, a.z);
+}
 __global__ void __launch_bounds__(kJoinThreads) tree_mla_join_kernel(const TreeParams p) {
   __shared__ Joined part[kJoinThreads];
+  __shared__ Cut cuts[kJoinThreads];
+  __shared__ int sums[kJoinWarps], found, found_at;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // launched under the end of the main kernel: its results first
-  const Cut cut = p.cuts[blockIdx.x];
-  if (!cut.pieces) return;
-  const int D = kLat / p.halves, D8 = D / 8;   // output features per slot row
-  const int split = cut.pieces >= 8 ? 4 : 1, width = kJoinThreads / split;
-  const int group = threadIdx.x / width, id = threadIdx.x % width;
-  const int team = blockIdx.x / p.halves, rank = blockIdx.x % p.halves;
-  const int64_t stride = static_cast<int64_t>(p.halves) * 2 * p.M * (D + 2);
-  const float* next = part_slot(p, static_cast<int64_t>(team) * p.halves + rank, 0);   // slot 0 of this team
-  const float* first = part_slot(p, static_cast<int64_t>(team) * p.halves + rank, 1);
-  const int count = cut.rows * D8;
-  for (int e0 = blockIdx.y * width; e0 < count; e0 += kJoinY * width) {
-    // neighbours in memory are neighbours in the CTA: features of a row, or rows
-    const int e = min(e0 + id, count - 1);
-    const int c = p.halves == 1 ? e / D8 : e % cut.rows, d = p.halves == 1 ? e % D8 : e / cut.rows;
-    const int at = p.halves == 1 ? c * D + d * 8 : (d * p.M + c) * 8;
-    const int at_m = p.M * D + c, at_z = at_m + p.M;
-    Joined a{{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, -INFINITY, 0.f};
-    // two pieces at a time (an item has at least two): their loads are in flight together
-    for (int i = group; i <= cut.pieces; i += 2 * split) {
-      float m[2], z[2];
-      float4 x[2][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D8 = kLat / p.halves / 8;
+  const Cut own = p.cuts[blockIdx.x];
+  Cut mine{0, 0, 0};                           // thread ↔ CTA of the main kernel
+  if (threadIdx.x < gridDim.x) mine = p.cuts[threadIdx.x];
+  if (own.pieces < kJoinSplit && own.pieces > 0)
+    for (int unit = blockIdx.y * kJoinWarps + warp; unit * 32 < own.rows * D8; unit += kJoinY * kJoinWarps) {
+      const Unit u = join_unit(p, own, blockIdx.x, unit, lane);
+      Joined a = join_pieces<2>(u.run, 0, 1, own.pieces);
+      join_store(p, own, u, a);
+    }
+  if (!__syncthreads_or(mine.pieces >= kJoinSplit)) return;
+  cuts[threadIdx.x] = mine;
+  const int units = mine.pieces >= kJoinSplit ? (mine.rows * D8 + 31) / 32 : 0;
+  int end = units;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int piece = min(i + h * split, cut.pieces);
-        const float* s = piece == 0 ? first : next + piece * stride;   // 0: this team's slot 1; then the next teams' slot 0
-        m[h] = s[at_m];
-        z[h] = s[at_z];
-        x[h][0] = *reinterpret_cast<const float4*>(s + at);
-        x[h][1] = *reinterpret_cast<const float4*>(s + at + 4);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, end, o);
+    if (lane >= o) end += v;
+  }
+  if (lane == 31) sums[warp] = end;
+  __syncthreads();
+  int total = 0;
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (w < warp) end += sums[w];
+    total += sums[w];
+  }
+  for (int j = blockIdx.y * gridDim.x + blockIdx.x; j < total; j += gridDim.x * kJoinY) {
+    if (end - units <= j && j < end) {
+      found = threadIdx.x;
+      found_at = j - (end - units);
+    }
+    __syncthreads();
+    const Cut cut = cuts[found];
+    const Unit u = join_unit(p, cut, found, found_at, lane);
+    Joined a = join_pieces<4>(u.run, warp, kJoinWarps, cut.pieces);
+    part[threadIdx.x] = a;
+    __syncthreads();
+    if (warp == 0) {
+      for (int g = 1; g < kJoinWarps; ++g) {
+        const Joined& b = part[g * 32 + lane];
+        join_add(a, b.top, b.z, b.o);
       }
-      join_add(a, m[0], z[0], reinterpret_cast<const float*>(x[0]));
-      if (i + split <= cut.pieces) join_add(a, m[1], z[1], reinterpret_cast<const float*>(x[1]));
+      join_store(p, cut, u, a);
     }
-    if (split > 1) {
-      part[threadIdx.x] = a;
-      __syncthreads();
-      if (group == 0)
-        for (int g = 1; g < split; ++g) {
-          const Joined& b = part[g * width + id];
-          join_add(a, b.top, b.z, b.o);
-        }
-      __syncthreads();
-    }
-    if (group == 0 && e0 + id < count) {
-      const float inv = a.z == 0.f ? 0.f : 1.f / a.z;
-      const int64_t to = (cut.row0 + c) * kLat + rank * D + d * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a.o[i] *= inv;
-      if (p.out_bf16) {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to) =
-            make_uint4(bf_pack(a.o[0], a.o[1]), bf_pack(a.o[2], a.o[3]), bf_pack(a.o[4], a.o[5]), bf_pack(a.o[6], a.o[7]));
-      } else {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + to);
-        dst[0] = make_float4(a.o[0], a.o[1], a.o[2], a.o[3]);
-        dst[1] = make_float4(a.o[4], a.o[5], a.o[6], a.o[7]);
-      }
-      if (p.lse && d == 0 && rank == 0) p.lse[cut.row0 + c] = lse_of(a.top, a.z);
-    }
+    __syncthreads();
   }
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // How a call's rows and tiles are dealt.  Rows that share keys: up to 64 go to the
-// transposed kernel above with the fewest columns that hold them (16, 32, 64);
-// more to the wide kernel (tree_mla_wide.cu) in groups of 128, two CTAs each.
+// transposed kernel above with the fewest columns that hold them (16, 32, 64; 16
+// heads over 16 x 30 000 positions: 113 us with 16 columns, 121 with 32; 32 rows over
+// 32 x 16 000: 129 with 32, 166 with 64); more to the wide kernel (tree_mla_wide.cu) in
+// groups of 128, two CTAs each (128 tokens of 64 heads, 2 048 of 16 000 positions:
+// 113 us here, 127 there; of 128 heads 139 there, 204 here in two groups).
 struct Plan {
   int M, halves, teams, whole;
   size_t part_bytes, ws;
 };
 Plan plan_for(int n, int H, int max_len, int k, int sms) {
   Plan pl;
+  sms = sms < kJoinThreads ? sms : kJoinThreads;   // (the join has a thread per CTA)
   const int64_t rows = k ? H : static_cast<int64_t>(n) * H;
   pl.M = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   pl.halves = pl.M == 128 ? 2 : 1;
   pl.teams = sms / pl.halves > 0 ? sms / pl.halves : 1;
   const int64_t keys = k ? static_cast<int64_t>(k) + n : max_len;
-  pl.whole = keys <= kMinShare || pl.teams == 1;
+  pl.whole = keys <= 2 * kMinShare || pl.teams == 1;
   const size_t ctas = static_cast<size_t>(pl.teams) * pl.halves;
   pl.part_bytes = ctas * 2 * pl.M * (kLat / pl.halves + 2) * sizeof(float);
   pl.ws = pl.whole ? 0 : pl.part_bytes + ctas * sizeof(Cut);

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
         fence_proxy_async_smem();              // the copies wrote through the generic proxy
         if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
-        if (p.fault && tiles == 1 && !(ok = waits(&ms.never, 0))) break;
+        if (p.fault && c == n - 1 && !(ok = waits(&ms.never, 0))) break;
         tc_fence_after();
         if (elect_one()) {
           int x = xs;
