@@ -269,6 +269,23 @@ def test_row_counts_of_every_kernel(n, H, page, ctxs, cnts, k, tree):
     check_tree(out, lse, q64, paged, real, SCALE, mask, idx, untouched=5.0)
 
 
+@pytest.mark.parametrize("H", [3, 20, 64, 100, 200])
+@pytest.mark.parametrize("ctxs", [[6000, 130, 1300, 0, 9000], [12000], [700, 900, 800], [256, 257]])
+def test_items_of_few_and_many_pieces(H, ctxs):
+    """Contexts cut into one piece, a few, or one for most SMs, side by side; the
+    join's order is fixed, so two calls give the same bits."""
+    from sparse_attention_token_idx_b200 import binding as X
+    rng = np.random.default_rng(H + len(ctxs))
+    B = len(ctxs)
+    paged = Paged(rng, [c + 1 for c in ctxs], 64).fill(rng)
+    q64, q = bf(rng.standard_normal((B, 1, H, DIM)))
+    for dtype in (torch.bfloat16, torch.float32):
+        out, lse = _run(X, paged, q, [1] * B, 1, dtype=dtype)
+        check_tree(out, lse, q64, paged, [1] * B, SCALE)
+        again, lse2 = _run(X, paged, q, [1] * B, 1, dtype=dtype)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("H", [4, 30, 128])
 @pytest.mark.parametrize("scale", [3.0, -0.3])
 def test_reference_maximum_rises_in_every_kernel(H, scale):
