@@ -28,7 +28,7 @@
 //                in TMEM is rescaled); P = 2^(s − m) in bf16 in shared memory;
 //                between pieces they put the next queries' first six chunks into
 //                TMEM while the last product runs;
-//   warp 19      asks for the tiles' lines in L2 a few tiles ahead of the copies (the
+//   warp 19      asks for the tiles' rows in L2 a few tiles ahead of the copies (the
 //                rings hold a tile and a half, less than the latency of HBM).
 // Rounding, bounded waits and the way out as in tree_mla.cu.
 #include "tree_mla.cuh"
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kPrefetchWarp) {
     // ================================================================ prefetch
     // this CTA's half of the rows, one bulk request each (128 x 2 048 selected positions
-    // of 16 384, 128 heads: 139 us, 149 without the warp; 128 x 8 drafted heads over
+    // of 16 384, 128 heads: 139 us, 149 without the warp; 8 drafts of 128 heads over
     // 32 x 8 192: 332 and 345)
     const uint8_t* from = reinterpret_cast<const uint8_t*>(p.cache);
     for (int tiles = 0;; ++tiles) {
