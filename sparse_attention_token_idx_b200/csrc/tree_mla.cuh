@@ -453,9 +453,39 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
       cut.pieces = sh.size >= s.tiles ? 1 : (s.tiles - t1 + static_cast<int>(sh.size) - 1) / static_cast<int>(sh.size);
     }
     const int nkeys = p.indices ? p.k : s.ctx;
+    // Its tiles' keys, lane ↔ keys E·lane …: the positions of tile t + 2 and the page
+    // numbers of tile t + 1 are fetched while tile t is published, and those of the
+    // first two before anything else of the piece (0.1 - 0.3 us off a short call)
+    const int32_t* sel = p.indices ? p.indices + (static_cast<int64_t>(b) * p.n + tok) * p.k : nullptr;
+    const int32_t* pages = p.table + static_cast<int64_t>(b) * p.max_pages;
+    uint64_t any = 0;                         // drafts that some row sees
+    auto page_of = [&](int pos) {
+      return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.div_mul >> p.div_shift);
+    };
+    auto position = [&](int t, int e) {       // position of a key, −1 (or beyond the context) where it selects nothing
+      const int v = t * KT + E * lane + e;
+      if (v >= nkeys) return v - nkeys < s.cnt ? s.ctx + v - nkeys : -1;
+      if (!sel) return v;
+      return t < t1 ? __ldg(sel + v) : -1;
+    };
+    auto valid = [&](int t, int e, int pos) {  // a selection names context positions only
+      return pos >= 0 && (t * KT + E * lane + e >= nkeys || pos < s.ctx);
+    };
+    auto seen = [&](int t, int e) {
+      const int v = t * KT + E * lane + e - nkeys;
+      return v < 0 || v >= 64 || ((any >> v) & 1);
+    };
+    int pos_next[E], page_next[E], pos_far[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      pos_next[e] = position(t0, e);
+      if (!valid(t0, e, pos_next[e])) pos_next[e] = -1;
+      pos_far[e] = position(t0 + 1, e);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) page_next[e] = pos_next[e] >= 0 ? __ldg(pages + page_of(pos_next[e])) : 0;
     const int pb = pieces & 1;
     if (pieces >= 2 && !(ok = waits.nap(&ms.piece_empty[pb], ((pieces >> 1) - 1) & 1))) break;
-    uint64_t any = 0;
     for (int c = lane; c < M; c += 32) {
       const uint64_t m = c < rows ? draft_mask(p, b, p.indices ? tok : quotient(lo + c, p.H), s.cnt) : 0;
       ms.mask[pb][c] = m;
@@ -475,31 +505,10 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms.piece_full[pb]);
-    // ---- its tiles: lane ↔ keys E·lane …  The positions of tile t + 2 and the
-    // page numbers of tile t + 1 are fetched while tile t is published
-    const int32_t* sel = p.indices ? p.indices + (static_cast<int64_t>(b) * p.n + tok) * p.k : nullptr;
-    const int32_t* pages = p.table + static_cast<int64_t>(b) * p.max_pages;
-    auto page_of = [&](int pos) {
-      return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.div_mul >> p.div_shift);
-    };
-    auto position = [&](int t, int e) {       // position of a key, −1 where it selects nothing
-      const int v = t * KT + E * lane + e;
-      if (v >= nkeys) return v - nkeys < s.cnt && ((any >> (v - nkeys)) & 1) ? s.ctx + v - nkeys : -1;
-      if (!sel) return v;
-      return t < t1 ? __ldg(sel + v) : -1;
-    };
-    auto valid = [&](int t, int e, int pos) {  // a selection names context positions only
-      return pos >= 0 && (t * KT + E * lane + e >= nkeys || pos < s.ctx);
-    };
-    int pos_next[E], page_next[E], pos_far[E];
+    // ---- its tiles
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      pos_next[e] = position(t0, e);
-      if (!valid(t0, e, pos_next[e])) pos_next[e] = -1;
-      pos_far[e] = position(t0 + 1, e);
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) page_next[e] = pos_next[e] >= 0 ? __ldg(pages + page_of(pos_next[e])) : 0;
+    for (int e = 0; e < E; ++e)
+      if (!seen(t0, e)) pos_next[e] = -1;
     for (int t = t0; t < t1; ++t) {
       int row[E];
       uint32_t kinds = 0;
@@ -521,7 +530,7 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
       if (t + 1 < t1) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          pos_next[e] = valid(t + 1, e, pos_far[e]) ? pos_far[e] : -1;
+          pos_next[e] = valid(t + 1, e, pos_far[e]) && seen(t + 1, e) ? pos_far[e] : -1;
           page_next[e] = pos_next[e] >= 0 ? __ldg(pages + page_of(pos_next[e])) : 0;
           pos_far[e] = position(t + 2, e);
         }
