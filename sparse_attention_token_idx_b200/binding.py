@@ -372,7 +372,7 @@ def _args(what: str, dev: int, *args):
         if t is None:
             out.append(None)
             continue
-        if t.dtype not in dtypes or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        if t.get_device() != dev or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
             _refuse(what, name, t, dtypes, shape, dev, False)
         out.append(t.data_ptr())
     if dev < 0:
@@ -391,6 +391,9 @@ class _On:
         self.device, self.given, self.contexts = device, stream, ()
 
     def __enter__(self):
+        if self.given is None and _current_device() == self.device:
+            self.stream = _current_stream(self.device)
+            return self
         contexts = []
         if torch.cuda.current_device() != self.device:
             contexts.append(torch.cuda.device(self.device))
@@ -408,6 +411,15 @@ class _On:
         for c in reversed(self.contexts):
             c.__exit__(*exc)
         return False
+
+
+# (after the first CUDA tensor, so that the runtime is up)
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _current_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 _F32 = (torch.float32,)
@@ -434,24 +446,26 @@ def latent_append(kv_proj, gain, eps: float, rope_cos, rope_sin, positions, page
                          "page_table [B, max_pages], q_pe [B, n, H, 64]")
     if q_pe is None and q_out is not None:
         raise ValueError("latent_append: q_out without q_pe")
-    B, n = kv_proj.shape[:2]
-    pages, page_size, max_pages = cache.shape[0], cache.shape[1], page_table.shape[1]
+    B, n, _ = kv_proj.shape
+    pages, page_size, _ = cache.shape
+    max_pages = page_table.shape[1]
     row = LATENT + ROTARY
     H = 0 if q_pe is None else q_pe.shape[2]
     dev = kv_proj.get_device()
     tables = (B, n, ROTARY // 2)
     # the two strided arguments: element pitches, 0 for a dimension of one entry
-    if kv_proj.dtype not in _BF16 or kv_proj.shape != (B, n, row) or kv_proj.stride(2) != 1:
+    kb, kt, last = kv_proj.stride()
+    if kv_proj.dtype not in _BF16 or kv_proj.shape != (B, n, row) or last != 1:
         _refuse(what, "kv_proj", kv_proj, _BF16, (B, n, row), dev, True)
-    kb, kt = kv_proj.stride(0) if B > 1 else 0, kv_proj.stride(1) if n > 1 else 0
+    kb, kt = kb if B > 1 else 0, kt if n > 1 else 0
     qp, qb, qt, qh = None, 0, 0, 0
     if q_pe is not None:
-        if q_pe.dtype not in _BF16 or q_pe.shape != (B, n, H, ROTARY) or q_pe.stride(3) != 1 or \
-                q_pe.get_device() != dev:
+        qb, qt, qh, last = q_pe.stride()
+        if q_pe.dtype not in _BF16 or q_pe.shape != (B, n, H, ROTARY) or last != 1 or q_pe.get_device() != dev:
             _refuse(what, "q_pe", q_pe, _BF16, (B, n, H, ROTARY), dev, True)
         if H:
-            qp, qh = q_pe.data_ptr(), q_pe.stride(2) if H > 1 else 0
-            qb, qt = q_pe.stride(0) if B > 1 else 0, q_pe.stride(1) if n > 1 else 0
+            qp = q_pe.data_ptr()
+        qb, qt, qh = qb if B > 1 else 0, qt if n > 1 else 0, qh if H > 1 else 0
     g, cos, sin, pos, cnt, tab, c, qo = _args(
         what, dev, ("gain", gain, _F32, (LATENT,)), ("rope_cos", rope_cos, _F32, tables),
         ("rope_sin", rope_sin, _F32, tables), ("positions", positions, _I32, (B,)), ("counts", counts, _I32, (B,)),
@@ -489,10 +503,11 @@ def tree_mla(q, cache, page_table, lengths, softmax_scale: float, *, max_len: in
     if q.dim() != 4 or cache.dim() != 3 or page_table.dim() != 2 or (indices is not None and indices.dim() != 3):
         raise ValueError("tree_mla: q [B, n, H, 576], cache [num_pages, page_size, 576], page_table [B, max_pages], "
                          "indices [B, n, k]")
-    B, n, H = q.shape[:3]
+    B, n, H, _ = q.shape
     if n > MAX_DRAFTS:
         raise ValueError(f"tree_mla: at most {MAX_DRAFTS} rows per sequence")
-    pages, page_size, max_pages = cache.shape[0], cache.shape[1], page_table.shape[1]
+    pages, page_size, _ = cache.shape
+    max_pages = page_table.shape[1]
     row = LATENT + ROTARY
     k = 0
     if indices is not None:
