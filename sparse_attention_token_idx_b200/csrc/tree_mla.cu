@@ -14,8 +14,10 @@
 // K = 16 costs 40 / 41 / 48 cycles at N = 16 / 32 / 64 (shared-memory reads of
 // A, 4 KB, and B; the tensor cores alone need 8 / 16 / 32), so a 128-key tile
 // costs 68 MMAs ≈ 2 700 – 3 300 cycles, against 147 KB of cache rows that HBM
-// delivers to one SM in about 6 500: small N is bound by HBM, N = 64 by the MMAs
-// and the shared-memory bandwidth that they take.
+// delivers to one SM in about 5 700.  Rows from HBM bind small N (16 x 131 000
+// positions, 16 heads: 86% of its rate); rows from L2 leave the chain of one tile, its
+// last copy, scores, softmax and product, 5 400 cycles, since shared memory holds one
+// tile and a quarter.
 //
 // One CTA, 15 warps (23 for N = 64):
 //   warp 0     the planner (tree_mla.cuh);
@@ -30,8 +32,8 @@
 //              for selected rows in L2 ahead of the copies was measured, up to four tiles
 //              ahead, by lines and by rows: 5 – 10% less time where HBM is idle (16 x 7
 //              tokens), up to 17% more where it is not (128 tokens with rows of their own).)
-//              A key set's rows are read by this CTA alone, so they are the first to
-//              leave L2: 128 tokens of 2 048 rows 84 -> 74 us, 16 x 131 000 positions
+//              A key set's rows are read by one CTA (tokens of a sequence may share
+//              selected rows), so they are the first to leave L2: 128 tokens of 2 048 rows 84 -> 74 us, 16 x 131 000 positions
 //              242 -> 239; in the wide kernel, where two CTAs read them, 139 -> 150;
 //   warps 7 …  softmax: thread ↔ (key, part of the rows).  Scores are compared with
 //              a running reference maximum per row as it is; only where one passes it
