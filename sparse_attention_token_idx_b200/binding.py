@@ -8,6 +8,7 @@ the device is not an sm_100 GPU, the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -380,37 +381,14 @@ def _args(what: str, dev: int, *args):
     return out
 
 
-class _On:
+@contextlib.contextmanager
+def _on(device: int, stream):
     """The device of a call's tensors as the current one, and its stream (None: the
-    device's current stream) as the current one for what the call allocates;
-    .stream is its handle.  Does nothing where both are so already."""
-
-    __slots__ = ("device", "given", "stream", "contexts")
-
-    def __init__(self, device: int, stream):
-        self.device, self.given, self.contexts = device, stream, ()
-
-    def __enter__(self):
-        if self.given is None and _current_device() == self.device:
-            self.stream = _current_stream(self.device)
-            return self
-        contexts = []
-        if torch.cuda.current_device() != self.device:
-            contexts.append(torch.cuda.device(self.device))
-        if self.given is not None:
-            if self.given.device.index != self.device:
-                raise IdxError(f"the stream is on cuda:{self.given.device.index}, the tensors on cuda:{self.device}")
-            contexts.append(torch.cuda.stream(self.given))
-        for c in contexts:
-            c.__enter__()
-        self.contexts = contexts
-        self.stream = torch._C._cuda_getCurrentRawStream(self.device)
-        return self
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
-        return False
+    device's current stream) as the current one for what the call allocates."""
+    if stream is not None and stream.device.index != device:
+        raise IdxError(f"the stream is on cuda:{stream.device.index}, the tensors on cuda:{device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
 
 
 # (after the first CUDA tensor, so that the runtime is up)
@@ -471,12 +449,16 @@ def latent_append(kv_proj, gain, eps: float, rope_cos, rope_sin, positions, page
         ("rope_sin", rope_sin, _F32, tables), ("positions", positions, _I32, (B,)), ("counts", counts, _I32, (B,)),
         ("page_table", page_table, _I32, (B, max_pages)), ("cache", cache, _BF16, (pages, page_size, row)),
         ("q_out", q_out, _BF16, (B, n, H, row)))
-    with _On(dev, stream) as on:
-        if H and q_out is None:
-            q_out = torch.empty((B, n, H, row), dtype=torch.bfloat16, device=kv_proj.device)
-            qo = q_out.data_ptr()
-        code = load().idx_latent_append(kv_proj.data_ptr(), kb, kt, g, eps, cos, sin, 1 if interleaved else 0, pos, cnt, tab, max_pages,
-                                        B, n, c, pages, page_size, qp, qb, qt, qh, H, qo if H else None, on.stream)
+    if stream is not None or _current_device() != dev:
+        with _on(dev, stream):
+            return latent_append(kv_proj, gain, eps, rope_cos, rope_sin, positions, page_table, cache,
+                                 interleaved=interleaved, counts=counts, q_pe=q_pe, q_out=q_out)
+    if H and q_out is None:
+        q_out = torch.empty((B, n, H, row), dtype=torch.bfloat16, device=kv_proj.device)
+        qo = q_out.data_ptr()
+    code = load().idx_latent_append(kv_proj.data_ptr(), kb, kt, g, eps, cos, sin, 1 if interleaved else 0, pos, cnt, tab,
+                                    max_pages, B, n, c, pages, page_size, qp, qb, qt, qh, H, qo if H else None,
+                                    _current_stream(dev))
     if code:
         _check(code, "idx_latent_append")
     return q_out
@@ -523,22 +505,25 @@ def tree_mla(q, cache, page_table, lengths, softmax_scale: float, *, max_len: in
         ("counts", counts, _I32, (B,)), ("tree_mask", tree_mask, _BITS64, (B, n)), ("indices", indices, _I32, (B, n, k)),
         ("out", out, _OUT, (B, n, H, LATENT)), ("lse", lse, _F32, (B, n, H)),
         ("ws", ws, _U8, None if ws is None else ws.shape))
+    if stream is not None or _current_device() != dev:
+        with _on(dev, stream):                   # what is allocated belongs to the call's stream
+            return tree_mla(q, cache, page_table, lengths, softmax_scale, max_len=max_len, counts=counts,
+                            tree_mask=tree_mask, indices=indices, out=out, lse=lse, ws=ws)
     lib = load()
-    with _On(dev, stream) as on:                 # what is allocated here belongs to the call's stream
-        if out is None:
-            out = torch.empty((B, n, H, LATENT), dtype=torch.bfloat16, device=q.device)
-            op = out.data_ptr()
-        if lse is None:
-            lse = torch.empty((B, n, H), dtype=torch.float32, device=q.device)
-            lp = lse.data_ptr()
-        if ws is None:
-            need = lib.idx_tree_mla_workspace_size(B, n, H, max_len, k)
-            if need:
-                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-                wp = ws.data_ptr()
-        code = lib.idx_tree_mla(qp, c, tab, max_pages, pages, page_size, ln, cnt, B, n, H, max_len, mask, idx, k,
-                                softmax_scale, op, OUT_BF16 if out.dtype is torch.bfloat16 else OUT_F32, lp, wp,
-                                0 if ws is None else ws.numel(), on.stream)
+    if out is None:
+        out = torch.empty((B, n, H, LATENT), dtype=torch.bfloat16, device=q.device)
+        op = out.data_ptr()
+    if lse is None:
+        lse = torch.empty((B, n, H), dtype=torch.float32, device=q.device)
+        lp = lse.data_ptr()
+    if ws is None:
+        need = lib.idx_tree_mla_workspace_size(B, n, H, max_len, k)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            wp = ws.data_ptr()
+    code = lib.idx_tree_mla(qp, c, tab, max_pages, pages, page_size, ln, cnt, B, n, H, max_len, mask, idx, k,
+                            softmax_scale, op, OUT_BF16 if out.dtype is torch.bfloat16 else OUT_F32, lp, wp,
+                            0 if ws is None else ws.numel(), _current_stream(dev))
     if code:
         _check(code, "idx_tree_mla")
     return out, lse
