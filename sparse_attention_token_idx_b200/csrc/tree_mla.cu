@@ -697,15 +697,20 @@ struct Plan {
   int M, halves, teams, whole;
   size_t part_bytes, ws;
 };
-Plan plan_for(int n, int H, int max_len, int k, int sms) {
+Plan plan_for(int B, int n, int H, int max_len, int k, int sms) {
   Plan pl;
   sms = sms < kJoinThreads ? sms : kJoinThreads;   // (the join has a thread per CTA)
   const int64_t rows = k ? H : static_cast<int64_t>(n) * H;
   pl.M = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   pl.halves = pl.M == 128 ? 2 : 1;
-  pl.teams = sms / pl.halves > 0 ? sms / pl.halves : 1;
   const int64_t keys = k ? static_cast<int64_t>(k) + n : max_len;
-  pl.whole = keys <= 2 * kMinShare || pl.teams == 1;
+  const int most = sms / pl.halves > 0 ? sms / pl.halves : 1;
+  pl.whole = keys <= 2 * kMinShare || most == 1;
+  // no more teams than the call can have shares (one sequence of 2 048 positions, 64
+  // heads: 17.7 us with 16 CTAs, 19.1 with 148, most of them for nothing)
+  const int64_t items = (k ? n : 1) * ((rows + pl.M - 1) / pl.M) * B;
+  const int64_t per_item = pl.whole ? 1 : (keys + kMinShare - 1) / kMinShare;
+  pl.teams = items < most && items * per_item < most ? static_cast<int>(items * per_item) : most;
   const size_t ctas = static_cast<size_t>(pl.teams) * pl.halves;
   pl.part_bytes = ctas * 2 * pl.M * (kLat / pl.halves + 2) * sizeof(float);
   pl.ws = pl.whole ? 0 : pl.part_bytes + ctas * sizeof(Cut);
@@ -727,7 +732,8 @@ int launch(const CUtensorMap& tq, const TreeParams& p, int ctas, cudaStream_t st
 using namespace idx;
 extern "C" size_t idx_tree_mla_workspace_size(int B, int n, int H, int max_len, int k) {
   if (B <= 0 || n <= 0 || n > IDX_MAX_DRAFTS || H <= 0 || max_len <= 0 || k < 0) return 0;
-  return plan_for(n, H, max_len, k, num_sms()).ws;
+  if (static_cast<int64_t>(B) * n > 0x7FFFFFFF / H) return 0;     // (idx_tree_mla refuses it)
+  return plan_for(B, n, H, max_len, k, num_sms()).ws;
 }
 
 extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int32_t* page_table, int max_pages,
@@ -753,7 +759,7 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
     return IDX_ERR_ALIGN;
   const int64_t rows = static_cast<int64_t>(B) * n;
   if (rows > kMaxRows / H) return IDX_ERR_SHAPE;
-  const Plan pl = plan_for(n, H, max_len, k, num_sms());
+  const Plan pl = plan_for(B, n, H, max_len, k, num_sms());
   if (pl.ws > 0 && !ws) return IDX_ERR_NULL;
   if (ws_bytes < pl.ws) return IDX_ERR_SCRATCH;
   const int ctas = pl.teams * pl.halves;

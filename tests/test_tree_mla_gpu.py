@@ -286,6 +286,30 @@ def test_items_of_few_and_many_pieces(H, ctxs):
         assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("B,n,H,ctx,k", [
+    (1, 1, 16, 300, 0), (1, 1, 3, 129, 0), (2, 3, 20, 700, 0), (1, 2, 64, 2000, 0), (1, 1, 128, 5000, 0),
+    (3, 4, 128, 400, 0), (1, 2, 16, 900, 300), (2, 5, 128, 900, 260), (60, 1, 16, 500, 0), (1, 1, 16, 40000, 0),
+])
+def test_workspace_of_exactly_the_stated_size(B, n, H, ctx, k):
+    """The call needs no byte more than it says, and writes none behind."""
+    from sparse_attention_token_idx_b200 import binding as X
+    rng = np.random.default_rng(B * 100 + H)
+    paged = Paged(rng, [max(n, ctx - 37 * b) + n for b in range(B)], 64).fill(rng)
+    q64, q = bf(rng.standard_normal((B, n, H, DIM)))
+    idx = None
+    if k:
+        idx = np.stack([[rng.choice(paged.lens[b] - n, k, replace=False) for _ in range(n)] for b in range(B)]).astype(np.int32)
+    need = X.tree_mla_workspace_size(B, n, H, max(paged.lens), k)
+    assert (need > 0) == ((k + n if k else max(paged.lens)) > 256)    # up to 256 keys stay whole
+    room = torch.full((need + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = _run(X, paged, q, [n] * B, n, indices=idx, given=False, ws=room[:need])
+    assert bool((room[need:] == 0xA5).all())
+    check_tree(out, lse, q64, paged, [n] * B, SCALE, None, idx)
+    if need:
+        with pytest.raises(X.IdxError):
+            _run(X, paged, q, [n] * B, n, indices=idx, given=False, ws=room[:need - 16])
+
+
 @pytest.mark.parametrize("H", [4, 30, 128])
 @pytest.mark.parametrize("scale", [3.0, -0.3])
 def test_reference_maximum_rises_in_every_kernel(H, scale):
