@@ -509,8 +509,10 @@ IDX_API int idx_e4m3_encode(const float* x, int64_t count, uint8_t* out, idx_str
  * Fault-injection control for tests: when `flags` has bit 0 set, the next score
  * and idx_tree_mla launches make one bounded wait in each CTA wait for a barrier
  * that nothing signals, with the wait budget set to `budget_ns`; the kernels then
- * report IDX_DEV_ERR_TIMEOUT and return.  idx_debug_set(0, 0) restores normal
- * operation (2 s wait budget).
+ * report IDX_DEV_ERR_TIMEOUT and return.  Bit 2: in idx_tree_mla launches, one of
+ * the softmax warps that share rows waits so where its CTA's work has ended (its
+ * results are written by then).  idx_debug_set(0, 0) restores normal operation (2 s
+ * wait budget).
  */
 IDX_API void idx_debug_set(unsigned int flags, unsigned long long budget_ns);
 

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       for (int c = 0; c < n && ok; ++c) {
         // Sᵀ = K · qᵀ, once the softmax has read the last S, chunk by chunk as they land
         if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
-        if (p.fault && c == n - 1 && !(ok = waits(&ms.never, 0))) break;
+        if ((p.fault & kFaultScores) && c == n - 1 && !(ok = waits(&ms.never, 0))) break;
         // (the rotary chunk first where its place is free since the last scores, so that
         // less follows the last copy; last where P held it)
         const int rs = tiles % C::kRopes;
@@ -351,7 +351,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       const int pb = pieces & 1;
       if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
       const Piece pc = ms.piece[pb];
-      if (pc.t0 == pc.t1) break;
+      if (pc.t0 == pc.t1) {                                // the end of the list
+        if ((p.fault & kFaultEnd) && quad == 0) ok = waits(&ms.never, 0);
+        break;
+      }
       float m = -INFINITY;                                 // reference maximum of column my_col, log2 units
       float l[NC];                                         // sums of this key's weights, before their rounding
 #pragma unroll
@@ -537,7 +540,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       }
       ++pieces;
     }
-    if (!ok && !gone) meeting.leave();
+    if (!gone) meeting.part(ok);
   }
   // ------------------------------------------------------------ teardown
   tc_fence_before();
@@ -799,7 +802,7 @@ extern "C" int idx_tree_mla(const uint16_t* q, const uint16_t* cache, const int3
   p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(ws) + pl.part_bytes);
   const DebugState dbg = debug_state();
   p.budget_ns = dbg.budget_ns;
-  p.fault = dbg.flags & 1;
+  p.fault = dbg.flags & (kFaultScores | kFaultEnd);
   p.err = device_error_word();
   if (!p.err) return check_launch();
   auto* s = reinterpret_cast<cudaStream_t>(stream);

@@ -35,6 +35,8 @@ constexpr int kMinShare = 128;
 constexpr int kAhead = 4;                     // tiles that the planner may be ahead of its readers
 constexpr float kRaise = 8.f;                 // log2 margin of the reference maximum
 constexpr float kNone = -3.0e38f;             // stands for a reference maximum of −inf: any score passes it
+constexpr int kFaultScores = 1;               // the scores of a piece's last tile
+constexpr int kFaultEnd = 4;                  // one of the softmax warps that share rows, at its list's end
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Piece {                                // what the CTA does next: tiles [t0, t1) of an item
@@ -71,7 +73,7 @@ struct TreeParams {
   float* part;                                // [CTA][2] partial slots: M · (512 / halves) outputs, M maxima, M sums
   Cut* cuts;                                  // [CTA]
   unsigned long long budget_ns;               // bound of every wait
-  int fault;                                  // tests: the scores of a piece's last tile wait for a barrier that nothing signals
+  int fault;                                  // tests: who waits for a barrier that nothing signals
   unsigned int* err;
 };
 
@@ -181,10 +183,13 @@ __device__ __forceinline__ bool bar_named_any(int id, int count, bool v) {
   return r != 0;
 }
 // The softmax warps that share rows meet at one named barrier, always by vote().
-// The meetings are not bounded in time, so a warp that gives up leaves: it writes
-// the number of the next meeting and takes its place there once more, saying true;
-// the others see the number and go too.  (A warp can give up only between
-// meetings that end a wait; the number tells this meeting from a later one.)
+// The meetings are not bounded in time, so every warp takes its place once more on
+// its way out (part): one that gives up writes the number of that meeting first and
+// says true, and the others, wherever they then meet, see the number and go too.
+// The meeting after the list's end is there for a warp that gave up while the
+// others came to the end: all of them have met equally often, so its last meeting
+// is theirs.  (A warp can give up only between meetings that end a wait; the number
+// tells this meeting from a later one.)
 struct Meeting {
   int id, count, number;
   volatile int* left_at;
@@ -193,9 +198,9 @@ struct Meeting {
     return bar_named_any(id, count, v);
   }
   __device__ __forceinline__ bool left() const { return __any_sync(0xFFFFFFFFu, *left_at == number); }
-  __device__ __forceinline__ void leave() {
-    *left_at = number + 1;
-    vote(true);
+  __device__ __forceinline__ void part(bool ok) {
+    if (!ok) *left_at = number + 1;
+    vote(!ok);
   }
 };
 

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
         fence_proxy_async_smem();              // the copies wrote through the generic proxy
         if (tiles >= 1 && !(ok = waits(&ms.s_free, (tiles - 1) & 1))) break;
-        if (p.fault && c == n - 1 && !(ok = waits(&ms.never, 0))) break;
+        if ((p.fault & kFaultScores) && c == n - 1 && !(ok = waits(&ms.never, 0))) break;
         tc_fence_after();
         if (elect_one()) {
           int x = xs;
@@ -353,7 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok) {
       const int pb = pieces & 1;
       const Piece pc = ms.piece[pb];
-      if (pc.t0 == pc.t1) break;
+      if (pc.t0 == pc.t1) {                                // the end of the list
+        if ((p.fault & kFaultEnd) && part == 0) ok = waits(&ms.never, 0);
+        break;
+      }
       const uint64_t drafts = ms.mask[pb][r_id];
       float m = -INFINITY, l = 0.f;                        // reference maximum (log2 units), sum of this half's weights
       // what this row sees of a tile's keys: the context, and its drafts (draft j is
@@ -538,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++pieces;
     }
-    if (!ok && !gone) meeting.leave();
+    if (!gone) meeting.part(ok);
   }
   // ------------------------------------------------------------ teardown
   tc_fence_before();
