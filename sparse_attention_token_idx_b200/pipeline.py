@@ -30,13 +30,30 @@ class Indexer:
         self.k_scale_cache = torch.zeros((B, T_cap), dtype=torch.uint8 if self.e8m0 else torch.float32,
                                          device=self.device)
         self._bufs = {}
+        self._projections = None                # of the last step_hidden
 
     def _buf(self, name, shape, dtype):
+        """Scratch kept for the next step of the same shape."""
         t = self._bufs.get(name)
         if t is None or t.shape != shape or t.dtype != dtype:
             t = torch.empty(shape, dtype=dtype, device=self.device)
             self._bufs[name] = t
         return t
+
+    def _own(self, stream):
+        """Allocates for one call, on its stream: inside a capture the memory is the
+        graph's and stays so as long as the graph."""
+        def new(name, shape, dtype):
+            with torch.cuda.stream(stream):
+                return torch.empty(shape, dtype=dtype, device=self.device)
+        return new
+
+    def _scratch(self, stream):
+        """Where a step's scratch comes from.  A step that is being captured keeps
+        nothing that an eager step of another shape would replace, and shares nothing
+        with another graph."""
+        with torch.cuda.stream(stream):
+            return self._own(stream) if torch.cuda.is_current_stream_capturing() else self._buf
 
     def append(self, k_new: torch.Tensor, positions: torch.Tensor, stream=None):
         """Rotate, quantise and store k_new [B, n, 128] bf16 at slots positions[b] …"""
@@ -53,17 +70,18 @@ class Indexer:
         cache; e8m0 storage quantises the two sets apart), then score + top-k
         (fused, or scorer + top-k through the workspace for prefill shapes)."""
         B, n = q.shape[0], q.shape[1]
-        q_fp8 = self._buf("q_fp8", tuple(q.shape), torch.uint8)
-        w = self._buf("w", tuple(w_raw.shape), torch.float32)
+        buf = self._scratch(stream)
+        q_fp8 = buf("q_fp8", tuple(q.shape), torch.uint8)
+        w = buf("w", tuple(w_raw.shape), torch.float32)
         if self.e8m0:   # queries, then keys with byte scales: two launches
             X.quant_queries(q, w_raw, self.fmt, q_fp8, w, stream=stream)
             X.quant_append_e8(k_new, positions, self.k_cache, self.k_scale_cache, stream=stream)
         else:
             X.quant_queries_append(q, w_raw, k_new, positions, self.k_cache, self.k_scale_cache, self.fmt, q_fp8, w,
                                    stream=stream)
-        out = out if out is not None else self._buf("idx", (B, n, self.k), torch.int32)
+        out = out if out is not None else buf("idx", (B, n, self.k), torch.int32)
         ws_bytes = X.workspace_size(B, n, max_len, self.k)
-        ws = self._buf("ws", (ws_bytes,), torch.uint8) if ws_bytes else None
+        ws = buf("ws", (ws_bytes,), torch.uint8) if ws_bytes else None
         return X.score_topk_ex(q_fp8, w, self.k_cache, self.k_scale_cache, lengths, causal, self.k, max_len,
                                out=out, ws=ws, stream=stream)
 
@@ -77,13 +95,14 @@ class Indexer:
         if self.e8m0:
             raise ValueError("step_front writes fp32 key scales")
         B, n = k_proj.shape[0], k_proj.shape[1]
-        q_fp8 = self._buf("q_fp8", tuple(q_proj.shape), torch.uint8)
-        w = self._buf("w", tuple(w_raw.shape), torch.float32)
+        buf = self._scratch(stream)
+        q_fp8 = buf("q_fp8", tuple(q_proj.shape), torch.uint8)
+        w = buf("w", tuple(w_raw.shape), torch.float32)
         X.front_quant_append(q_proj, w_raw, k_proj, rope_cos, rope_sin, ln_gain, ln_bias, ln_eps, positions,
                              self.k_cache, self.k_scale_cache, self.fmt, q_fp8, w, stream=stream)
-        out = out if out is not None else self._buf("idx", (B, n, self.k), torch.int32)
+        out = out if out is not None else buf("idx", (B, n, self.k), torch.int32)
         ws_bytes = X.workspace_size(B, n, max_len, self.k)
-        ws = self._buf("ws", (ws_bytes,), torch.uint8) if ws_bytes else None
+        ws = buf("ws", (ws_bytes,), torch.uint8) if ws_bytes else None
         return X.score_topk_ex(q_fp8, w, self.k_cache, self.k_scale_cache, lengths, causal, self.k, max_len,
                                out=out, ws=ws, stream=stream)
 
@@ -96,11 +115,13 @@ class Indexer:
         B, n = x.shape[0], x.shape[1]
         T = B * n
         hidden, q_lora = x.shape[2], qr.shape[2]
-        q_proj = self._buf("q_proj", (B, n, X.HEADS, X.DIM), torch.bfloat16)
-        k_proj = self._buf("k_proj", (B, n, X.DIM), torch.bfloat16)
-        w_raw = self._buf("w_raw", (B, n, X.HEADS), torch.float32)
+        buf = self._scratch(stream)
+        q_proj = buf("q_proj", (B, n, X.HEADS, X.DIM), torch.bfloat16)
+        k_proj = buf("k_proj", (B, n, X.DIM), torch.bfloat16)
+        w_raw = buf("w_raw", (B, n, X.HEADS), torch.float32)
+        self._projections = q_proj, k_proj, w_raw
         need = X.project_workspace_size(T, hidden, q_lora)
-        ws = self._buf("proj_ws", (need,), torch.uint8)
+        ws = buf("proj_ws", (need,), torch.uint8)
         X.project(x.reshape(T, hidden), qr.reshape(T, q_lora), wq_b, wk, w_proj, q_out=q_proj.view(T, X.HEADS, X.DIM),
                   k_out=k_proj.view(T, X.DIM), w_out=w_raw.view(T, X.HEADS), ws=ws, stream=stream)
         return self.step_front(q_proj, w_raw, k_proj, rope_cos, rope_sin, ln_gain, ln_bias, positions, lengths,
@@ -111,27 +132,29 @@ class Indexer:
         lengths[b] cached keys (n ≤ lengths[b] ≤ max_len), nothing appended: what
         the rows of a drafted tree attend to in their context (every row sees all of
         it; the drafts themselves are LatentCache.attend's).  q [B, n, 64, 128] bf16,
-        w_raw [B, n, 64] fp32."""
+        w_raw [B, n, 64] fp32.  The result, where `out` is not given, and the scratch
+        are this call's own: steps take turns with selections of other row counts."""
         B, n = q.shape[0], q.shape[1]
-        q_fp8 = self._buf("q_fp8", tuple(q.shape), torch.uint8)
-        w = self._buf("w", tuple(w_raw.shape), torch.float32)
+        buf = self._own(stream)
+        q_fp8 = buf("q_fp8", tuple(q.shape), torch.uint8)
+        w = buf("w", tuple(w_raw.shape), torch.float32)
         X.quant_queries(q, w_raw, self.fmt, q_fp8, w, stream=stream)
-        out = out if out is not None else self._buf("idx", (B, n, self.k), torch.int32)
+        out = out if out is not None else buf("idx", (B, n, self.k), torch.int32)
         ws_bytes = X.workspace_size(B, n, max_len, self.k)
-        ws = self._buf("ws", (ws_bytes,), torch.uint8) if ws_bytes else None
+        ws = buf("ws", (ws_bytes,), torch.uint8) if ws_bytes else None
         return X.score_topk_ex(q_fp8, w, self.k_cache, self.k_scale_cache, lengths, False, self.k, max_len, out=out,
                                ws=ws, stream=stream)
 
     def projections(self):
         """(q_proj, k_proj, w_raw) of the last step_hidden."""
-        return self._bufs["q_proj"], self._bufs["k_proj"], self._bufs["w_raw"]
+        return self._projections
 
     def capture(self, k_new, q, w_raw, positions, lengths, *, causal: bool, max_len: int, out=None):
         """Record one step on static input tensors into a CUDA graph; returns
         (graph, out) — replay the graph after refilling the inputs in place.
         The step also runs once, for real, before the capture (warm-up)."""
         if out is None:
-            out = self._buf("idx_graph", (q.shape[0], q.shape[1], self.k), torch.int32)
+            out = torch.empty((q.shape[0], q.shape[1], self.k), dtype=torch.int32, device=self.device)
         s = torch.cuda.Stream(device=self.device)
         s.wait_stream(torch.cuda.current_stream(self.device))
         with torch.cuda.stream(s):                      # warm-up outside the capture
