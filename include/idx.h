@@ -100,8 +100,8 @@ enum idx_status_code {
 /* Bits of the device error word (returned by idx_device_error_bits). */
 #define IDX_DEV_ERR_TIMEOUT 0x1u  /* a bounded wait inside a kernel gave up */
 #define IDX_DEV_ERR_POSITION 0x2u /* idx_quant_append: positions[b] < 0 or positions[b] + n > T_cap */
-#define IDX_DEV_ERR_LENGTH 0x4u   /* score/top-k: lengths[b] < n or lengths[b] > max_len; the paged calls: a count or
-                                     a length out of range */
+#define IDX_DEV_ERR_LENGTH 0x4u   /* score/top-k: lengths[b] < n (< 0 where causal = 0) or > max_len; the paged calls:
+                                     a count or a length out of range */
 #define IDX_DEV_ERR_PAGE 0x8u     /* the paged calls: a page number outside [0, num_pages) */
 
 /*
@@ -224,8 +224,11 @@ IDX_API int idx_project(const uint16_t* x, const uint16_t* qr, int64_t tokens, i
  * with the causal mask of the Indexer.forward excerpt.
  *   q_fp8  [B, n, 64, 128] e4m3 codes; w [B, n, 64] folded weights (idx_quant_queries).
  *   k_cache [B, T_cap, 128], k_scale_cache [B, T_cap]; lengths [B] int32.
- *   max_len: host-side upper bound on lengths[b] (n ≤ max_len ≤ min(T_cap, IDX_MAX_LEN));
- *            it sizes the launch.
+ *   causal = 1: the n rows are the sequence's last n keys, row i sees the keys up
+ *            to its own: n ≤ lengths[b].  causal = 0: every row sees all lengths[b]
+ *            keys, be they more than n, fewer or none (rows that are not cached).
+ *   max_len: host-side upper bound on lengths[b], at least n (1 where causal = 0)
+ *            and at most min(T_cap, IDX_MAX_LEN); it sizes the launch.
  *   scores [B, n, ld] float32 out: S for visible keys, −inf for every other column < ld.
  *          ld ≥ 1; columns ≥ ld are not computed.
  * q_fp8 and k_cache must be 16-byte aligned (they are read by TMA).

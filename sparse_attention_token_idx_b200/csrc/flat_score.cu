@@ -94,7 +94,7 @@ struct Block {
     b = item / p.ntb;
     row0 = (item - b * p.ntb) * NT;
     len = p.lengths[b];
-    bad = len < p.n || len > p.max_len;
+    bad = len < (p.causal ? p.n : 0) || len > p.max_len;
   }
   __device__ __forceinline__ int vis(const FlatParams& p, int row) const {   // keys row `row` sees
     return (row < p.n && !bad) ? (p.causal ? len - p.n + row + 1 : len) : 0;

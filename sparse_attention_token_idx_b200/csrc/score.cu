@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(Cfg<NT, FUSED, STAGES, NUM_ACC, EPI_WARPS, TSP
     if (G == 1) issue_first(ceil_div(p.max_len, kTileKeys), 0);
   }
   const int len = p.lengths[b];
-  const bool bad = len < p.n || len > p.max_len;
+  const bool bad = len < (p.causal ? p.n : 0) || len > p.max_len;
   if (bad && rank == 0 && threadIdx.x == 0) raise_error(p.err, IDX_DEV_ERR_LENGTH);
 
   // visible keys of row j of this block (0 for rows past n or a bad length)
@@ -583,8 +583,9 @@ int check_score_args(const uint8_t* q_fp8, const float* w, const uint8_t* k_cach
   if (B < 0 || n < 0 || T_cap <= 0) return IDX_ERR_SHAPE;
   if (B == 0 || n == 0) return IDX_OK;
   if (!q_fp8 || !w || !k_cache || !k_scale_cache || !lengths) return IDX_ERR_NULL;
-  if (max_len < n || max_len > T_cap || max_len > IDX_MAX_LEN) return IDX_ERR_SHAPE;
   if (causal != 0 && causal != 1) return IDX_ERR_SHAPE;
+  // (without the causal mask the rows need not be cached themselves)
+  if (max_len < (causal ? n : 1) || max_len > T_cap || max_len > IDX_MAX_LEN) return IDX_ERR_SHAPE;
   if ((reinterpret_cast<uintptr_t>(q_fp8) | reinterpret_cast<uintptr_t>(k_cache) |
        reinterpret_cast<uintptr_t>(k_scale_cache)) & 15)
     return IDX_ERR_ALIGN;

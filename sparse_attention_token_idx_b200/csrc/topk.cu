@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kTopkThreads, 1) topk_kernel(const TopkParams 
   const int b = static_cast<int>(row / p.n);
   const int i = static_cast<int>(row - static_cast<int64_t>(b) * p.n);
   const int len = p.lengths[b];
-  const bool bad = len < p.n || len > p.max_len;
+  const bool bad = len < (p.causal ? p.n : 0) || len > p.max_len;
   if (bad && rank == 0 && threadIdx.x == 0 && i == 0) raise_error(p.err, IDX_DEV_ERR_LENGTH);
   const int vis = bad ? 0 : (p.causal ? len - p.n + i + 1 : len);
   const int chunk = vis > 0 ? (vis + G - 1) / G : 0;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) topk_row_kernel(const RowParam
   const int b = static_cast<int>(row / p.n);
   const int i = static_cast<int>(row - static_cast<int64_t>(b) * p.n);
   const int len = p.lengths[b];
-  const bool bad = len < p.n || len > p.max_len;
+  const bool bad = len < (p.causal ? p.n : 0) || len > p.max_len;
   if (bad && tid == 0 && i == 0) raise_error(p.err, IDX_DEV_ERR_LENGTH);
   const int vis = bad ? 0 : (p.causal ? len - p.n + i + 1 : len);
   int32_t* out = p.indices + row * p.k;
@@ -469,7 +469,7 @@ extern "C" int idx_topk(const float* scores, const int32_t* lengths, int B, int 
   if (B == 0 || n == 0) return IDX_OK;
   if (!scores || !lengths || !indices) return IDX_ERR_NULL;
   if (causal != 0 && causal != 1) return IDX_ERR_SHAPE;
-  if (max_len < n || max_len > IDX_MAX_LEN || static_cast<int64_t>(max_len) > ld) return IDX_ERR_SHAPE;
+  if (max_len < (causal ? n : 1) || max_len > IDX_MAX_LEN || static_cast<int64_t>(max_len) > ld) return IDX_ERR_SHAPE;
   const int64_t rows = static_cast<int64_t>(B) * n;
   const int sms = num_sms();
   // one CTA per row when the row fits a CTA and enough rows cover the GPU:

@@ -129,12 +129,14 @@ class Indexer:
 
     def select(self, q, w_raw, lengths, *, max_len: int, out=None, stream=None):
         """Top-k positions [B, n, k] int32 of n query rows per sequence over its first
-        lengths[b] cached keys (n ≤ lengths[b] ≤ max_len), nothing appended: what
+        lengths[b] cached keys (0 ≤ lengths[b] ≤ max_len), nothing appended: what
         the rows of a drafted tree attend to in their context (every row sees all of
-        it; the drafts themselves are LatentCache.attend's).  q [B, n, 64, 128] bf16,
+        it, a context shorter than k is selected whole; the drafts themselves are
+        LatentCache.attend's).  q [B, n, 64, 128] bf16,
         w_raw [B, n, 64] fp32.  The result, where `out` is not given, and the scratch
         are this call's own: steps take turns with selections of other row counts."""
         B, n = q.shape[0], q.shape[1]
+        max_len = max(max_len, 1)               # (no sequence has any context yet)
         buf = self._own(stream)
         q_fp8 = buf("q_fp8", tuple(q.shape), torch.uint8)
         w = buf("w", tuple(w_raw.shape), torch.float32)
