@@ -109,9 +109,36 @@ __device__ __forceinline__ float reduce_columns(float* v, int lane) {
   return r;
 }
 
+// Draft j's row at `at` of the four latent buffers from `first` on: zeros where it is not finite
+__device__ __forceinline__ void clear_wild(uint8_t* at, int first, int buffers, unsigned long long* wild, int j) {
+  auto piece = [&](int i) {
+    const int b = first + (i >> 4);
+    return reinterpret_cast<uint4*>(at + (b < buffers ? b : b - buffers) * kPair + ((i >> 3) & 1) * kChunk + (i & 7) * 16);
+  };
+  bool any = false;
+  for (int i = 0; i < 64; ++i) any |= not_finite(*piece(i));
+  if (!any) return;
+  atomicOr(wild, 1ull << j);
+  for (int i = 0; i < 64; ++i) *piece(i) = make_uint4(0, 0, 0, 0);
+}
+// NaN into outputs key, 128 + key … of columns [c0, c0 + nc) that see a wild draft, where its features are not finite
+__device__ __noinline__ void spoil_columns(const TreeParams& p, const Piece& pc, const uint64_t* mask, uint64_t wild,
+                                           int key, int c0, int nc) {
+  for (; wild; wild &= wild - 1) {
+    const int j = __ffsll(static_cast<long long>(wild)) - 1;
+    const uint16_t* src = draft_row(p, pc, j);
+    for (int d = key; d < kLat; d += kTile) {
+      if (!not_finite(src[d])) continue;
+      for (int c = c0; c < min(c0 + nc, pc.rows); ++c)
+        if ((mask[c] >> j) & 1)
+          spoil(p, pc, c, d, pc.slot < 0 ? nullptr : part_slot(p, blockIdx.x, pc.slot) + c * kLat + d);
+    }
+  }
+}
+
 template <int N>
 __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
-    tree_mla_kernel(const __grid_constant__ CUtensorMap tmap_q, const TreeParams p) {
+    tree_mla_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ TreeParams p) {
   using C = Cfg<N>;
   constexpr int NC = C::kNC;
   extern __shared__ uint8_t smem_raw[];
@@ -351,10 +378,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       const int pb = pieces & 1;
       if (!(ok = waits(&ms.piece_full[pb], (pieces >> 1) & 1))) break;
       const Piece pc = ms.piece[pb];
-      if (pc.t0 == pc.t1) {                                // the end of the list
-        if ((p.fault & kFaultEnd) && quad == 0) ok = waits(&ms.never, 0);
-        break;
-      }
+      if (pc.t0 == pc.t1) break;
       float m = -INFINITY;                                 // reference maximum of column my_col, log2 units
       float l[NC];                                         // sums of this key's weights, before their rounding
 #pragma unroll
@@ -462,27 +486,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
           *reinterpret_cast<uint4*>(p_row + ((part_id * NC / 8 + c) ^ (key & 7)) * 16) =
               make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         // a draft's row that only some columns see must not reach the others as
-        // 0 · NaN: where it is not finite it becomes zero (the columns that see
-        // it have it in their weights already)
+        // 0 · NaN: where it is not finite it becomes zero (see spoil for the columns
+        // that see it)
         if (pc.mixed && drafts && part_id == 0) {
           for (int u = 0; u < 4 && ok; ++u)
             ok = waits(&ms.pair_full[(pairs + u) % C::kPairs], ((pairs + u) / C::kPairs) & 1);
           if (!ok) break;
-          if (kind >= 2) {
-            bool wild = false;
-            for (int j = 0; j < 64; ++j) {
-              const uint4 x = *reinterpret_cast<const uint4*>(smem + ((pairs + (j >> 4)) % C::kPairs) * kPair +
-                                                              ((j >> 3) & 1) * kChunk + key * 128 + (j & 7) * 16);
-              const uint32_t e[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                wild |= (e[i] & 0x7F80u) == 0x7F80u || (e[i] & 0x7F800000u) == 0x7F800000u;
-            }
-            if (wild)
-              for (int j = 0; j < 64; ++j)
-                *reinterpret_cast<uint4*>(smem + ((pairs + (j >> 4)) % C::kPairs) * kPair + ((j >> 3) & 1) * kChunk +
-                                          key * 128 + (j & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
+          if (kind >= 2) clear_wild(smem + key * 128, pairs % C::kPairs, C::kPairs, &ms.wild[pb], kind - 2);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -532,6 +542,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
           }
         }
       }
+      if (const uint64_t wild = ms.wild[pb])
+        spoil_columns(p, ms.piece[pb], ms.mask[pb], wild, key, part_id * NC, NC);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -540,7 +552,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       }
       ++pieces;
     }
-    if (!gone) meeting.part(ok);
+    if (!gone) {
+      if (ok && (p.fault & kFaultEnd) && quad == 0) ok = waits(&ms.never, 0);
+      meeting.part(ok);
+    }
   }
   // ------------------------------------------------------------ teardown
   tc_fence_before();

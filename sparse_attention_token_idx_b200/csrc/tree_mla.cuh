@@ -325,6 +325,7 @@ __device__ __forceinline__ uint64_t draft_mask(const TreeParams& p, int b, int i
 template <int M, int KT, int kWarps>
 struct PlanState {
   uint64_t mask[2][M];                        // per piece parity: drafts each row sees
+  unsigned long long wild[2];                 // drafts that were taken out of V, their rows not being finite
   alignas(16) uint8_t kind[kAhead][KT];       // per tile (mod kAhead) and key: 0 unseen, 1 context, 2 + j draft j
   alignas(16) int row[kAhead][KT];            // cache rows of the keys, −1: none
   int last[kAhead];                           // no tile: the list has ended
@@ -507,6 +508,7 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
       pc.mixed = !p.indices && quotient(lo, p.H) != quotient(lo + rows - 1, p.H);
       pc.nkeys = nkeys;
       pc.row0 = row0;
+      ms.wild[pb] = 0;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms.piece_full[pb]);
@@ -577,6 +579,39 @@ __device__ __forceinline__ void plan(const TreeParams& p, State& ms, const Share
   }
   if (!p.whole && lane == 0) p.cuts[blockIdx.x] = cut;
   if (pieces) waits.drain(&ms.q_full, (pieces - 1) & 1);   // landed before the memory goes
+}
+
+// A draft whose latent features are not all finite, in a group of rows of which some
+// do not see it: it is taken out of V, since 0 · NaN would reach those rows too.
+// Rows that see it have its score, which is not finite either.  NaN and +∞ make
+// their weights NaN, and their sums say so; −∞ makes a weight of 0, and what
+// 0 · (what is not finite) would have put into the output is put there after the
+// product (spoil), where the draft's row is read once more.
+__device__ __forceinline__ bool not_finite(uint16_t bf) { return (bf & 0x7F80u) == 0x7F80u; }
+__device__ __forceinline__ bool not_finite(const uint4& x) {       // any of eight
+  const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+  bool r = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r |= (e[i] & 0x7F80u) == 0x7F80u || (e[i] & 0x7F800000u) == 0x7F800000u;
+  return r;
+}
+// cache row of draft j of the sequence that the group's first row belongs to; some
+// row sees it, so its page was one (checked again: the table is read anew)
+__device__ __forceinline__ const uint16_t* draft_row(const TreeParams& p, const Piece& pc, int j) {
+  const int64_t b = pc.row0 / (static_cast<int64_t>(p.n) * p.H);
+  const int pos = pc.nkeys + j, at = pos / p.page_size;
+  const int page = min(max(__ldg(p.table + b * p.max_pages + at), 0), p.num_pages - 1);
+  return p.cache + (static_cast<int64_t>(page) * p.page_size + (pos - at * p.page_size)) * kRow;
+}
+// NaN for output feature d of row `row0 + row`, or of a partial result (`part`: its place)
+__device__ __forceinline__ void spoil(const TreeParams& p, const Piece& pc, int row, int d, float* part) {
+  const float nan = __int_as_float(0x7FFFFFFF);
+  if (part)
+    *part = nan;
+  else if (p.out_bf16)
+    static_cast<__nv_bfloat16*>(p.out)[(pc.row0 + row) * kLat + d] = __float2bfloat16_rn(nan);
+  else
+    static_cast<float*>(p.out)[(pc.row0 + row) * kLat + d] = nan;
 }
 
 __device__ __forceinline__ float lse_of(float m, float z) {    // m in log2 units

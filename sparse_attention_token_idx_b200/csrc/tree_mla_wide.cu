@@ -74,8 +74,28 @@ __device__ __forceinline__ int feature_chunk(int pos, int half) {
   return pos < 4 ? 4 * (1 - half) + pos : pos == 4 ? 8 : 4 * half + pos - 5;
 }
 
+// 64 features of draft j: zeros where one of them is not finite
+__device__ __noinline__ void clear_wild(uint8_t* at, unsigned long long* wild, int j) {
+  uint4* x = reinterpret_cast<uint4*>(at);
+  bool any = false;
+  for (int i = 0; i < 8; ++i) any |= not_finite(x[i]);
+  if (!any) return;
+  atomicOr(wild, 1ull << j);
+  for (int i = 0; i < 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
+}
+// NaN into this thread's 128 outputs where a wild draft's features are not finite
+__device__ __noinline__ void spoil_half(const TreeParams& p, const Piece& pc, uint64_t wild, int r_id, int half, int part) {
+  for (; wild; wild &= wild - 1) {
+    const uint16_t* src = draft_row(p, pc, __ffsll(static_cast<long long>(wild)) - 1) + half * kHalf;
+    for (int c = part * (kHalf / 2); c < (part + 1) * (kHalf / 2); ++c)
+      if (not_finite(src[c]))
+        spoil(p, pc, r_id, half * kHalf + c,
+              pc.slot < 0 ? nullptr : part_slot(p, blockIdx.x, pc.slot) + (c >> 3) * 8 * kRows + r_id * 8 + (c & 7));
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_mla_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const TreeParams p) {
+    tree_mla_wide_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ TreeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   WideState& ms = *reinterpret_cast<WideState*>(smem + kOffMisc);
@@ -353,10 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok) {
       const int pb = pieces & 1;
       const Piece pc = ms.piece[pb];
-      if (pc.t0 == pc.t1) {                                // the end of the list
-        if ((p.fault & kFaultEnd) && part == 0) ok = waits(&ms.never, 0);
-        break;
-      }
+      if (pc.t0 == pc.t1) break;
       const uint64_t drafts = ms.mask[pb][r_id];
       float m = -INFINITY, l = 0.f;                        // reference maximum (log2 units), sum of this half's weights
       // what this row sees of a tile's keys: the context, and its drafts (draft j is
@@ -460,24 +477,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(p_row + ((part * 4 + c) ^ (r_id & 7)) * 16) =
               make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         // a draft's row that only some rows see must not reach the others as
-        // 0 · NaN: where it is not finite it becomes zero (the rows that see it
-        // have it in their sums already)
+        // 0 · NaN: where it is not finite it becomes zero (see spoil for the rows that
+        // see it)
         if (pc.mixed && pc.nkeys < (t + 1) * kKeys) {
           const int sl = tiles % kVs;
           if (!(ok = waits(&ms.v_full[sl], (tiles / kVs) & 1))) break;
           const int id = threadIdx.x - kFirstSoft * 32, key = id >> 2;
-          if (t * kKeys + key >= pc.nkeys) {               // (a key past the last draft is zeros)
-            uint4* x = reinterpret_cast<uint4*>(smem + sl * kV + (id & 3) * kChunk + key * 128);
-            bool wild = false;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t e[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) wild |= (e[i] & 0x7F80u) == 0x7F80u || (e[i] & 0x7F800000u) == 0x7F800000u;
-            }
-            if (wild)
-              for (int j = 0; j < 8; ++j) x[j] = make_uint4(0, 0, 0, 0);
-          }
+          if (t * kKeys + key >= pc.nkeys)                 // (a key past the last draft is zeros)
+            clear_wild(smem + sl * kV + (id & 3) * kChunk + key * 128, &ms.wild[pb], t * kKeys + key - pc.nkeys);
         }
         tc_fence_before();
         __syncwarp();
@@ -533,6 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      if (const uint64_t wild = ms.wild[pb] & ms.mask[pb][r_id])     // (no mask past the last row)
+        spoil_half(p, ms.piece[pb], wild, r_id, half, part);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -541,7 +550,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++pieces;
     }
-    if (!gone) meeting.part(ok);
+    if (!gone) {
+      if (ok && (p.fault & kFaultEnd) && part == 0) ok = waits(&ms.never, 0);
+      meeting.part(ok);
+    }
   }
   // ------------------------------------------------------------ teardown
   tc_fence_before();
