@@ -50,3 +50,28 @@ def test_refusals():
     with pytest.raises(ValueError):
         c.share(0, 1, 16)
     assert c.page_table.dtype == torch.int32
+
+
+def test_a_capture_on_the_caches_own_device_is_what_counts(monkeypatch):
+    """The check for a capture, and the upload, look at the cache's device and the
+    call's stream, whichever device is the current one."""
+    import contextlib
+    at = []
+
+    @contextlib.contextmanager
+    def entered(name, what):
+        at.append((name, what))
+        yield
+        at.pop()
+
+    c = LatentCache(1, 4, 16, 64, device="cpu")
+    monkeypatch.setattr(torch.cuda, "device", lambda d: entered("device", d))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: entered("stream", s))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: ("device", torch.device("cuda:3")) in at)
+    c.device = torch.device("cuda:3")
+    c.reserve(0, 16)
+    with pytest.raises(X.IdxError):
+        c.table()
+    assert (c.page_table == -1).all()                            # and the change is not forgotten
+    c.device = torch.device("cpu")
+    assert c.table()[0, 0] >= 0
