@@ -194,6 +194,7 @@ class LatentCache:
         self._users = [0] * num_pages
         self._free = list(range(num_pages - 1, -1, -1))
         self._stale = False
+        self._uploaded = None                    # event behind an upload that may still be under way
 
     def _held(self, b: int) -> list:
         if not 0 <= b < self.B:
@@ -243,17 +244,33 @@ class LatentCache:
         """The device page table, brought up to date (on `stream`, or the current one
         of its device) without waiting for it: what is uploaded is a pinned copy of the
         table as it is now (18 µs of the host's time for 128 sequences of 2 048 pages,
-        14 for 256 pages; row by row 18 for one row and 72 for eight)."""
-        if self._stale:
+        14 for 256 pages; row by row 18 for one row and 72 for eight).  Calls on other
+        streams are put behind the upload; replays of a graph are ordered by their user."""
+        if self._stale or self._uploaded is not None:
             if self.device.type != "cuda":
                 self.page_table.copy_(self._table)
-            else:
-                with torch.cuda.device(self.device), torch.cuda.stream(stream):
-                    if torch.cuda.is_current_stream_capturing():
+                self._stale = False
+                return self.page_table
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+                if self._stale:
+                    if capturing:
                         raise X.IdxError("LatentCache: the page table changed; call table() before the capture")
+                    self._wait_for_upload()                      # (one upload does not overtake another)
                     self.page_table.copy_(self._table.pin_memory(), non_blocking=True)
-            self._stale = False
+                    self._uploaded = torch.cuda.Event()
+                    self._uploaded.record()
+                    self._stale = False
+                elif not capturing:
+                    self._wait_for_upload()
         return self.page_table
+
+    def _wait_for_upload(self):
+        if self._uploaded is not None:
+            if self._uploaded.query():
+                self._uploaded = None
+            else:
+                torch.cuda.current_stream().wait_event(self._uploaded)
 
     def append(self, kv_proj, gain, eps, rope_cos, rope_sin, positions, *, interleaved=True, counts=None, q_pe=None,
                q_out=None, stream=None):

@@ -106,3 +106,32 @@ def test_shared_prefix_then_rows_of_ones_own():
             o, ls, bound, lerr = tree_row(q64[b, i], kv, 0.07)
             assert np.all(np.abs(out[b, i].double().cpu().numpy() - o) <= bound + UB * np.abs(o) * (1 + UB) + 1e-30)
             assert np.all(np.abs(lse[b, i].double().cpu().numpy() - ls) <= lerr)
+
+
+def test_calls_on_other_streams_come_behind_an_upload():
+    """The upload is asked for on a busy stream; a call on another stream reads the
+    table that it carries, and a second upload from there does not overtake it."""
+    from sparse_attention_token_idx_b200.pipeline import LatentCache
+    lc = LatentCache(4, 32, 64, 512)
+    busy, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for b in range(4):
+        lc.reserve(b, 64)
+    lc.table(busy)
+    lc.reserve(0, 128)
+    lc.table(other)                                              # (staging memory, kernels)
+    copy = torch.zeros_like(lc.page_table)
+    with torch.cuda.stream(other):
+        copy.copy_(lc.page_table)
+    torch.cuda.synchronize()
+    lc.reserve(1, 192)
+    want = lc._table.clone()
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(200_000_000)                           # about 0.1 s
+    lc.table(busy)
+    with torch.cuda.stream(other):
+        copy.copy_(lc.table())
+    lc.reserve(2, 256)
+    last = lc._table.clone()
+    lc.table(other)
+    torch.cuda.synchronize()
+    assert torch.equal(copy.cpu(), want) and torch.equal(lc.page_table.cpu(), last)
