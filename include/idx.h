@@ -430,6 +430,7 @@ enum idx_out_dtype { IDX_OUT_F32 = 0, IDX_OUT_BF16 = 1 };
  *            run at the same time need one each.
  * q, cache: 16-byte aligned; out, ws 32; tree_mask 8.  Scores and sums in fp32;
  * softmax_scale may be negative or 0; |softmax_scale| · log2 e must be finite in fp32.
+ * A score beyond 2^128 · ln 2 = 2.36e38 in size counts as infinite.
  * Errors: IDX_ERR_SHAPE, IDX_ERR_NULL, IDX_ERR_ALIGN, IDX_ERR_FMT (out_dtype),
  * IDX_ERR_SCRATCH.  counts[b] outside [0, n], lengths[b] < counts[b] or
  * lengths[b] > max_len raise IDX_DEV_ERR_LENGTH and leave the sequence's outputs as

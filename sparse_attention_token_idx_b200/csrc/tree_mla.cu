@@ -77,7 +77,7 @@ struct Cfg {
 template <int N>
 struct Misc : PlanState<N, kTile, Cfg<N>::kThreads / 32> {
   alignas(16) float wmax[Cfg<N>::kParts][4][Cfg<N>::kNC];   // row part, warp: column maxima
-  alignas(16) float m[Cfg<N>::kSoftWarps][Cfg<N>::kNC];     // reference maxima, a copy per softmax warp
+  alignas(16) float m[Cfg<N>::kSoftWarps][Cfg<N>::kNC];     // reference maxima (0 beyond kFar), a copy per softmax warp
   alignas(16) float alpha[Cfg<N>::kSoftWarps][Cfg<N>::kNC];
   alignas(16) float sum[Cfg<N>::kParts][4][Cfg<N>::kNC];
   uint64_t pair_full[5], pair_empty[5], rope_full[2], rope_empty[2];
@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       const Piece pc = ms.piece[pb];
       if (pc.t0 == pc.t1) break;
       float m = -INFINITY;                                 // reference maximum of column my_col, log2 units
+      bool check = true;                                   // first tile, or a column's maximum is beyond kFar
       float l[NC];                                         // sums of this key's weights, before their rounding
 #pragma unroll
       for (int c = 0; c < NC; ++c) l[c] = 0.f;
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         // Against the reference maxima as they are: only where some score passes
         // its column's by 2^8 (the first tile of a piece always) is there anything
         // to reduce; one barrier tells the part's four warps alike
-        bool over = t == pc.t0;
+        bool over = check;
         float far = -INFINITY;
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
@@ -438,12 +439,20 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
           float top = ms.wmax[part_id][0][my_col];
 #pragma unroll
           for (int w = 1; w < 4; ++w) top = fmaxf(top, ms.wmax[part_id][w][my_col]);
-          top = top == -INFINITY ? top : top * scale;
+          top = top == -INFINITY ? top : __fmul_rn(top, scale);
           const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
           const float a = !raise ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
           if (raise) m = top;
           ms.alpha[sw][my_col] = a;
-          ms.m[sw][my_col] = m == -INFINITY ? kNone : m;
+          ms.m[sw][my_col] = m == -INFINITY ? kNone : is_far(m) ? 0.f : m;
+          check = __any_sync(0xFFFFFFFFu, is_far(m));
+          if (check) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const float mc = __shfl_sync(0xFFFFFFFFu, m, c << kColShift);
+              if (is_far(mc)) z[c] = far_score(z[c], scale, mc);
+            }
+          }
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < NC; ++c) l[c] *= ms.alpha[sw][c];

@@ -34,7 +34,13 @@ constexpr int kLat = 512, kRow = 576;
 constexpr int kMinShare = 128;
 constexpr int kAhead = 4;                     // tiles that the planner may be ahead of its readers
 constexpr float kRaise = 8.f;                 // log2 margin of the reference maximum
-constexpr float kNone = -3.0e38f;             // stands for a reference maximum of −inf: any score passes it
+constexpr float kNone = -3.4028235e38f;       // stands for a reference maximum of −inf: any score passes it
+// A weight is 2^(s · scale − m), one fused operation, with m = fl(s_max · scale): what
+// that product was rounded by, half a step of m at most, multiplies all weights of a
+// row alike.  Beyond 2^28 (a step of 2^4 and more) that may be more than an exponent
+// holds, and scores that differ at all differ by 2^4: there the weight is 1 where
+// fl(s · scale) reaches m and 0 elsewhere.  Such rows are looked at in every tile.
+constexpr float kFar = 268435456.f;
 constexpr int kFaultScores = 1;               // the scores of a piece's last tile
 constexpr int kFaultEnd = 4;                  // one of the softmax warps that share rows, at its list's end
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -171,6 +177,12 @@ __device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
 // row's sum keeps it.
 __device__ __forceinline__ uint32_t bf_pack_weights(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo) + 0x8000u, __float_as_uint(hi) + 0x8000u, 0x7632);
+}
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar && m > -INFINITY; }
+// a score of a row beyond kFar as what stands in for it, with 0 for m: 0 or −inf (NaN where m is infinite)
+__device__ __forceinline__ float far_score(float z, float scale, float m) {
+  const float d = __fmul_rn(z, scale) - m;    // (not fused: m is such a product)
+  return d < 0.f ? -INFINITY : d;
 }
 // `count` threads meet; whether any of them says v
 __device__ __forceinline__ bool bar_named_any(int id, int count, bool v) {

@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pc.t0 == pc.t1) break;
       const uint64_t drafts = ms.mask[pb][r_id];
       float m = -INFINITY, l = 0.f;                        // reference maximum (log2 units), sum of this half's weights
+      bool check = true;                                   // first tile, or a row's maximum is beyond kFar
       // what this row sees of a tile's keys: the context, and its drafts (draft j is
       // key nkeys + j); read a tile ahead, while the last product runs
       uint32_t next_sees = 0;
@@ -424,23 +425,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c) far = fmaxf(far, z[c]);
         const float mu = m == -INFINITY ? kNone : m;
-        const bool raised = meeting.vote(t == pc.t0 || fmaf(far, scale, -mu) > kRaise);
+        const bool raised = meeting.vote(check || fmaf(far, scale, -mu) > kRaise);
         float a = 1.f;
         if (raised) {                                      // the same in both warps of these rows
           if ((gone = meeting.left())) break;
           ms.top[part][r_id] = far;
           meeting.vote(false);
           float top = fmaxf(far, ms.top[1 - part][r_id]);
-          top = top == -INFINITY ? top : top * scale;
+          top = top == -INFINITY ? top : __fmul_rn(top, scale);
           const bool raise = top > m + kRaise || (m == -INFINITY && top > -INFINITY);
           if (raise) {
             a = m == -INFINITY ? 0.f : ex2(m - top);
             m = top;
           }
           l *= a;
+          check = __any_sync(0xFFFFFFFFu, is_far(m));
+          if (is_far(m))
+#pragma unroll
+            for (int c = 0; c < 32; ++c) z[c] = far_score(z[c], scale, m);
           meeting.vote(false);                             // (top may be written again)
         }
-        const float base = m == -INFINITY ? kNone : m;
+        const float base = fabsf(m) > kFar ? 0.f : m;      // (−inf: the row has seen nothing, all its scores are −inf)
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
