@@ -388,7 +388,7 @@ IDX_API int idx_sparse_mla_decode(const uint16_t* q, const uint16_t* kv, const i
  * with counts[b] outside [0, n] IDX_DEV_ERR_LENGTH: neither writes anything (its
  * queries included).  A token whose page number is outside [0, num_pages)
  * raises IDX_DEV_ERR_PAGE and its cache row is not written.  Two tokens of a call
- * that share a slot leave one of their rows there, which one is not specified.
+ * that share a slot (of sequences that share its page) leave features of both there.
  */
 IDX_API int idx_latent_append(const uint16_t* kv_proj, int64_t kv_seq_pitch, int64_t kv_tok_pitch, const float* gain,
                               float eps, const float* rope_cos, const float* rope_sin, int interleaved,
@@ -428,7 +428,10 @@ enum idx_out_dtype { IDX_OUT_F32 = 0, IDX_OUT_BF16 = 1 };
  *            bytes, 32-byte aligned (may be NULL where that is 0).  It holds
  *            partial results inside the call: calls (or captured graphs) that may
  *            run at the same time need one each.
- * q, cache: 16-byte aligned; out, ws 32; tree_mask 8.  Scores and sums in fp32;
+ * q, cache: 16-byte aligned; out, ws 32; tree_mask 8.  Scores, the sum of the
+ * weights (lse), and the output's sums are fp32; the weights themselves are rounded
+ * to bf16 before they are multiplied with the rows, for the tensor cores: 2^-8 of
+ * each at most, which out carries in both of its types, IDX_OUT_F32 too.
  * softmax_scale may be negative or 0; |softmax_scale| · log2 e must be finite in fp32.
  * A score beyond 2^128 · ln 2 = 2.36e38 in size counts as infinite.
  * Errors: IDX_ERR_SHAPE, IDX_ERR_NULL, IDX_ERR_ALIGN, IDX_ERR_FMT (out_dtype),

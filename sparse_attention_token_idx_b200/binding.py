@@ -478,7 +478,8 @@ def tree_mla(q, cache, page_table, lengths, softmax_scale: float, *, max_len: in
     as they were.  tree_mask [B, n] int64: bit j of row i set where it sees draft j
     (None: a chain).  indices [B, n, k] int32: the context positions each row
     attends to (None: the whole context).  out bf16 or fp32 (allocated as bf16 when
-    None, its rows behind the counts unset), ws: uint8 workspace of
+    None, its rows behind the counts unset; in either type the softmax weights were
+    rounded to bf16 before the product, lse has them unrounded), ws: uint8 workspace of
     tree_mla_workspace_size bytes (allocated on the stream when None; calls that
     may overlap, captured graphs among them, need one each)."""
     what = "tree_mla"
