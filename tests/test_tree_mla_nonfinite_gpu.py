@@ -158,3 +158,23 @@ def test_rows_that_see_such_a_draft_alone(H, n):
     for i in range(n - 1):
         o, ls, bound, lerr = tree_row(q64[0, i], kv[[i]], SCALE)
         assert np.all(np.abs(out[0, i] - o) <= bound + 1e-30) and np.all(np.abs(lse[0, i] - ls) <= lerr)
+
+
+@pytest.mark.parametrize("H,n", [(10, 2), (16, 2), (10, 5), (16, 4), (8, 8), (20, 13)])
+def test_fp32_output_of_drafted_rows_under_a_tree(H, n):
+    """fp32 results of 17 to 64 rows (and more) that belong to several tokens, ragged,
+    each token with a mask of its own."""
+    from sparse_attention_token_idx_b200 import binding as X
+    from tests.paged_helpers import check_tree, random_tree
+    rng = np.random.default_rng(H * n)
+    ctxs, cnts = [1500, 0, 133, 260], [n, n - 1, n, 1]
+    paged = Paged(rng, [c + m for c, m in zip(ctxs, cnts)], 33).fill(rng)
+    q64, q = bf(rng.standard_normal((4, n, H, DIM)))
+    mask = [random_tree(rng, n) for _ in range(4)]
+    mask[2][n - 1] = 0
+    out = torch.full((4, n, H, LAT), 5.0, device="cuda")
+    lse = torch.full((4, n, H), 5.0, device="cuda")
+    X.tree_mla(q.cuda(), paged.cache_dev(), paged.table_dev(), dev(np.array(paged.lens, np.int32)), SCALE,
+               max_len=max(paged.lens), counts=dev(np.array(cnts, np.int32)), tree_mask=mask_dev(mask), out=out, lse=lse)
+    assert X.status() == (0, 0)
+    check_tree(out, lse, q64, paged, cnts, SCALE, mask, untouched=5.0)
