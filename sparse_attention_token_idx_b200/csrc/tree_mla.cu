@@ -579,8 +579,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
 // in CTA x's share, where it has few pieces.  Items of kJoinSplit pieces and more
 // (one long sequence over all SMs is one item) are dealt to all CTAs: one unit at a
 // time, whose pieces the CTA's eight warps share; their results are added in a
-// fixed order (64 heads over one sequence of 131 072: 69 us a call, 147 when CTA x
-// alone took its item).  Reads what the pieces wrote, from L2 as far as it is
+// fixed order (64 heads over one sequence of 131 072, L2 flushed before each call:
+// 69 us, 147 when CTA x alone took its item).  Reads what the pieces wrote, from L2 as far as it is
 // still there; two pieces of each of 128 items of 128 rows, 38 MB: 6 us.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinY = 8, kJoinSplit = 8;
 struct Joined {
@@ -718,8 +718,14 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // transposed kernel above with the fewest columns that hold them (16, 32, 64; 16
 // heads over 16 x 30 000 positions: 113 us with 16 columns, 121 with 32; 32 rows over
 // 32 x 16 000: 129 with 32, 166 with 64); more to the wide kernel (tree_mla_wide.cu) in
-// groups of 128, two CTAs each (128 tokens of 64 heads, 2 048 of 16 000 positions:
-// 113 us here, 127 there; of 128 heads 139 there, 204 here in two groups).
+// groups of 128, two CTAs each.  Both sides, the wide kernel and groups of 64 here, in us
+// in a CUDA graph:
+//   64 x 6 000 positions, one token of 65 / 96 / 128 / 144 / 160 / 192 / 256 heads:
+//     160 / 175 / 172 / 314 / 332 / 313 / 365 and 221 / 230 / 231 / 352 / 343 / 368 / 478;
+//   48 x 3 000, tokens of 16 heads, 5 / 6 / 8 / 9 / 10 / 13 / 16 of them:
+//     99 / 101 / 83 / 128 / 133 / 141 / 147 and 115 / 111 / 108 / 125 / 124 / 184 / 188.
+// (Groups of 64 win by 3 - 7% only at 144 and 160 rows of few keys, and the other way
+// round: 128 tokens of 64 heads, 2 048 of 16 000 positions take 113 us here, 127 there.)
 struct Plan {
   int M, halves, teams, whole;
   size_t part_bytes, ws;
@@ -734,7 +740,7 @@ Plan plan_for(int B, int n, int H, int max_len, int k, int sms) {
   const int most = sms / pl.halves > 0 ? sms / pl.halves : 1;
   pl.whole = keys <= 2 * kMinShare || most == 1;
   // no more teams than the call can have shares (one sequence of 2 048 positions, 64
-  // heads: 17.7 us with 16 CTAs, 19.1 with 148, most of them for nothing)
+  // heads, in a CUDA graph: 18.5 us with 16 CTAs, 19.9 with 148, most of them for nothing)
   const int64_t items = (k ? n : 1) * ((rows + pl.M - 1) / pl.M) * B;
   const int64_t per_item = pl.whole ? 1 : (keys + kMinShare - 1) / kMinShare;
   pl.teams = items < most && items * per_item < most ? static_cast<int>(items * per_item) : most;

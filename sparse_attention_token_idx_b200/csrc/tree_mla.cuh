@@ -28,9 +28,10 @@ namespace tree {
 
 constexpr int kLat = 512, kRow = 576;
 // Keys per share below which work is not split further: a tile of 128 keys (one
-// sequence of 2 048 positions, 64 heads: 24.6 us, with 256 32.8, with 512 37.9).  Up to
-// two of them an item stays whole, which saves the join's launch: 256 positions, 16
-// heads take 18.4 us then and 16.4 cut in two, 128 heads 20.5 and 24.6.
+// sequence of 2 048 positions, 64 heads, calls in a CUDA graph: 18.8 us, with 256 25.6,
+// with 512 31.2; 128 heads 19.7, 23.5, 26.8).  Up to two of them an item stays whole,
+// which saves the join's launch: 256 positions, 16 heads take 13.7 us then and 11.7
+// cut in two, 128 heads 16.8 and 17.9.
 constexpr int kMinShare = 128;
 constexpr int kAhead = 4;                     // tiles that the planner may be ahead of its readers
 constexpr float kRaise = 8.f;                 // log2 margin of the reference maximum

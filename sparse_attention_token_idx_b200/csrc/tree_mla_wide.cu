@@ -16,6 +16,9 @@
 // for this tile's softmax nor for its product, and the scores of tile t + 1 run while
 // the softmax of t does.  Scores and products are issued by two warps: what a warp asks of
 // a barrier waits behind the MMAs that it has queued (some 400 cycles of them).
+// Trees of 8 drafts of 128 heads over 32 x <= 8 192 positions: 2 460 cycles a tile, 14 500
+// from a piece's last tile to the next one's first, at 1.56 - 1.70 GHz under this load; of
+// a CTA's life 86% are inside pieces, 7.5% between them, 4.5% before the first scores.
 //
 // One CTA, 20 warps:
 //   warp 0       the planner (tree_mla.cuh);
