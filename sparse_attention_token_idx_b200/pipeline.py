@@ -136,6 +136,10 @@ class Indexer:
         w_raw [B, n, 64] fp32.  The result, where `out` is not given, and the scratch
         are this call's own: steps take turns with selections of other row counts."""
         B, n = q.shape[0], q.shape[1]
+        if B > self.B or q.shape != (B, n, X.HEADS, X.DIM) or w_raw.shape != q.shape[:3] or lengths.shape != (B,) or \
+                (out is not None and out.shape != (B, n, self.k)):
+            raise ValueError(f"Indexer.select: q [B, n, {X.HEADS}, {X.DIM}], w_raw [B, n, {X.HEADS}], lengths [B], "
+                             f"out [B, n, {self.k}], B at most {self.B}")
         max_len = max(max_len, 1)               # (no sequence has any context yet)
         buf = self._own(stream)
         q_fp8 = buf("q_fp8", tuple(q.shape), torch.uint8)

@@ -14,3 +14,19 @@ def test_bounds_that_are_refused(n, max_len, causal):
     assert lib.idx_score_topk(P16, P16, P16, P16, P16, 2, n, 64, max_len, causal, 8, P16, None, 0, None) == SHAPE
     assert lib.idx_score(P16, P16, P16, P16, P16, 2, n, 64, max_len, causal, P16, 64, None) == SHAPE
     assert lib.idx_topk(P16, P16, 2, n, 64, max_len, causal, 8, P16, None, 0, None) == SHAPE
+
+
+def test_select_refuses_shapes_that_are_not_its_caches():
+    import torch
+    from sparse_attention_token_idx_b200.pipeline import Indexer
+    ix = Indexer(2, 64, 0, 16, device="cpu")
+    z, bf, i32 = torch.zeros, torch.bfloat16, torch.int32
+
+    def select(q=(2, 3, 64, 128), w=(2, 3, 64), n=(2,), out=None):
+        return ix.select(z(q, dtype=bf), z(w), z(n, dtype=i32), max_len=64, out=out)
+
+    for kw in (dict(q=(3, 3, 64, 128), w=(3, 3, 64), n=(3,)), dict(q=(2, 3, 64, 128), w=(1, 3, 64)),
+               dict(q=(2, 3, 32, 128)), dict(q=(2, 3, 64, 64)), dict(w=(2, 64)), dict(w=(2, 2, 64)), dict(n=(3,)),
+               dict(n=(2, 1)), dict(out=z((2, 3, 8), dtype=i32)), dict(out=z((2, 2, 16), dtype=i32))):
+        with pytest.raises(ValueError):
+            select(**kw)
