@@ -29,31 +29,42 @@ class Indexer:
         self.k_cache = torch.zeros((B, T_cap, X.DIM), dtype=torch.uint8, device=self.device)
         self.k_scale_cache = torch.zeros((B, T_cap), dtype=torch.uint8 if self.e8m0 else torch.float32,
                                          device=self.device)
-        self._bufs = {}
+        self._bufs, self._on = {}, {}           # scratch by name, and the stream it belongs to
+        self._index = self.k_cache.get_device()
         self._projections = None                # of the last step_hidden
 
-    def _buf(self, name, shape, dtype):
-        """Scratch kept for the next step of the same shape."""
-        t = self._bufs.get(name)
-        if t is None or t.shape != shape or t.dtype != dtype:
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-            self._bufs[name] = t
-        return t
-
-    def _own(self, stream):
-        """Allocates for one call, on its stream: inside a capture the memory is the
-        graph's and stays so as long as the graph."""
-        def new(name, shape, dtype):
-            with torch.cuda.stream(stream):
-                return torch.empty(shape, dtype=dtype, device=self.device)
-        return new
-
-    def _scratch(self, stream):
-        """Where a step's scratch comes from.  A step that is being captured keeps
-        nothing that an eager step of another shape would replace, and shares nothing
-        with another graph."""
+    def _new(self, shape, dtype, stream):
+        """A tensor that belongs to the call's stream (inside a capture: to the graph)."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(stream):
-            return self._own(stream) if torch.cuda.is_current_stream_capturing() else self._buf
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _scratch(self, stream, whose: str = ""):
+        """Where a call's scratch comes from: kept by name for the next call of the
+        same shapes on the same stream.  A call that is being captured keeps nothing
+        that an eager call of another shape would replace, and shares nothing with
+        another graph: its scratch is the graph's, as long as the graph lives."""
+        if stream is None:
+            capturing = torch.cuda.is_current_stream_capturing()
+            on = X._current_stream(self._index) if self._index >= 0 else 0
+        else:
+            with torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+            on = stream.cuda_stream
+        if capturing:
+            return lambda name, shape, dtype: self._new(shape, dtype, stream)
+
+        bufs, streams = self._bufs, self._on
+
+        def kept(name, shape, dtype):
+            name = whose + name
+            t = bufs.get(name)
+            if t is None or t.shape != shape or streams[name] != on:   # (a name has one dtype)
+                bufs[name] = t = self._new(shape, dtype, stream)
+                streams[name] = on
+            return t
+        return kept
 
     def append(self, k_new: torch.Tensor, positions: torch.Tensor, stream=None):
         """Rotate, quantise and store k_new [B, n, 128] bf16 at slots positions[b] …"""
@@ -132,20 +143,22 @@ class Indexer:
         lengths[b] cached keys (0 ≤ lengths[b] ≤ max_len), nothing appended: what
         the rows of a drafted tree attend to in their context (every row sees all of
         it, a context shorter than k is selected whole; the drafts themselves are
-        LatentCache.attend's).  q [B, n, 64, 128] bf16,
-        w_raw [B, n, 64] fp32.  The result, where `out` is not given, and the scratch
-        are this call's own: steps take turns with selections of other row counts."""
-        B, n = q.shape[0], q.shape[1]
-        if B > self.B or q.shape != (B, n, X.HEADS, X.DIM) or w_raw.shape != q.shape[:3] or lengths.shape != (B,) or \
-                (out is not None and out.shape != (B, n, self.k)):
+        LatentCache.attend's).  q [B, n, 64, 128] bf16, w_raw [B, n, 64] fp32.  The
+        result, where `out` is not given, is a new tensor; none of the scratch is a
+        step's, so that steps and selections of other row counts take turns."""
+        shape = q.shape
+        B, n = shape[0], shape[1]
+        if B > self.B or shape != (B, n, X.HEADS, X.DIM) or w_raw.shape != (B, n, X.HEADS) or \
+                lengths.shape != (B,) or (out is not None and out.shape != (B, n, self.k)):
             raise ValueError(f"Indexer.select: q [B, n, {X.HEADS}, {X.DIM}], w_raw [B, n, {X.HEADS}], lengths [B], "
                              f"out [B, n, {self.k}], B at most {self.B}")
-        max_len = max(max_len, 1)               # (no sequence has any context yet)
-        buf = self._own(stream)
-        q_fp8 = buf("q_fp8", tuple(q.shape), torch.uint8)
-        w = buf("w", tuple(w_raw.shape), torch.float32)
+        if max_len < 1:
+            max_len = 1                         # (no sequence has any context yet)
+        buf = self._scratch(stream, "select ")
+        q_fp8 = buf("q_fp8", shape, torch.uint8)
+        w = buf("w", w_raw.shape, torch.float32)
         X.quant_queries(q, w_raw, self.fmt, q_fp8, w, stream=stream)
-        out = out if out is not None else buf("idx", (B, n, self.k), torch.int32)
+        out = out if out is not None else self._new((B, n, self.k), torch.int32, stream)
         ws_bytes = X.workspace_size(B, n, max_len, self.k)
         ws = buf("ws", (ws_bytes,), torch.uint8) if ws_bytes else None
         return X.score_topk_ex(q_fp8, w, self.k_cache, self.k_scale_cache, lengths, False, self.k, max_len, out=out,

@@ -69,7 +69,8 @@ def test_a_selection_and_a_step_of_one_shape_share_nothing(monkeypatch, n):
     select, sel = calls.storages(lambda: _select(ix, n))
     assert idx is not sel and not step & select
     again, sel2 = calls.storages(lambda: _select(ix, n))
-    assert sel2 is not sel and not again & select                # a result is the caller's to keep
+    assert sel2 is not sel                                       # a result is the caller's to keep
+    assert again & select == select - {sel.untyped_storage().data_ptr()}   # the scratch stays where it was
     assert calls.storages(lambda: _step(ix, n))[0] == step       # a step's scratch stays where it was
 
 
@@ -97,3 +98,18 @@ def test_projections_are_those_of_the_last_call(monkeypatch):
     calls.capturing = True
     graph, _ = calls.storages(lambda: _hidden(ix, 1))
     assert {t.untyped_storage().data_ptr() for t in ix.projections()} <= graph
+
+
+def test_scratch_belongs_to_one_stream(monkeypatch):
+    """A call on another stream does not take what a call on the first may still use."""
+    import contextlib
+    from types import SimpleNamespace
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    calls, ix = Calls(monkeypatch), Indexer(2, 64, 0, 16, device="cpu")
+    one, two = SimpleNamespace(cuda_stream=11), SimpleNamespace(cuda_stream=12)
+    a = _args(8)
+    used = [calls.storages(lambda: ix.select(**a, max_len=64, stream=s, out=torch.zeros((2, 8, 16), dtype=torch.int32)))[0]
+            for s in (one, one, two, two)]
+    out = [t.untyped_storage().data_ptr() for t in calls.seen if t.shape == (2, 8, 16)]
+    used = [u - set(out) for u in used]
+    assert used[0] == used[1] and used[2] == used[3] and not used[0] & used[2]
