@@ -30,6 +30,7 @@ class Indexer:
         self.k_scale_cache = torch.zeros((B, T_cap), dtype=torch.uint8 if self.e8m0 else torch.float32,
                                          device=self.device)
         self._bufs, self._on = {}, {}           # scratch by name, and the stream it belongs to
+        self.device = self.k_cache.device       # (with its number, whichever device is the current one later)
         self._index = self.k_cache.get_device()
         self._projections = None                # of the last step_hidden
 
@@ -205,6 +206,7 @@ class LatentCache:
         self.device = torch.device(device)
         self.max_pages = -(-max_len // page_size)
         self.cache = torch.zeros((num_pages, page_size, X.LATENT + X.ROTARY), dtype=torch.bfloat16, device=self.device)
+        self.device = self.cache.device          # (with its number, whichever device is the current one later)
         self.page_table = torch.full((B, self.max_pages), -1, dtype=torch.int32, device=self.device)
         self._table = torch.full((B, self.max_pages), -1, dtype=torch.int32)
         self._pages = [[] for _ in range(B)]

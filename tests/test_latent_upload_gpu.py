@@ -135,3 +135,12 @@ def test_calls_on_other_streams_come_behind_an_upload():
     lc.table(other)
     torch.cuda.synchronize()
     assert torch.equal(copy.cpu(), want) and torch.equal(lc.page_table.cpu(), last)
+
+
+def test_the_device_is_the_one_that_the_buffers_are_on():
+    """"cuda" is a number from the start: later calls may be made with another
+    device as the current one."""
+    from sparse_attention_token_idx_b200.pipeline import Indexer, LatentCache
+    now = torch.device("cuda", torch.cuda.current_device())
+    assert LatentCache(1, 4, 16, 64).device == now
+    assert Indexer(1, 64, 0, 8).device == now
