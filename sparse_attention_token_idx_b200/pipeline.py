@@ -153,6 +153,9 @@ class Indexer:
                 lengths.shape != (B,) or (out is not None and out.shape != (B, n, self.k)):
             raise ValueError(f"Indexer.select: q [B, n, {X.HEADS}, {X.DIM}], w_raw [B, n, {X.HEADS}], lengths [B], "
                              f"out [B, n, {self.k}], B at most {self.B}")
+        if self._index >= 0 and (stream is not None or X._current_device() != self._index):
+            with X._on(self._index, stream):
+                return self.select(q, w_raw, lengths, max_len=max_len, out=out)
         if max_len < 1:
             max_len = 1                         # (no sequence has any context yet)
         buf = self._scratch(stream, "select ")

@@ -30,3 +30,39 @@ def test_select_refuses_shapes_that_are_not_its_caches():
                dict(n=(2, 1)), dict(out=z((2, 3, 8), dtype=i32)), dict(out=z((2, 2, 16), dtype=i32))):
         with pytest.raises(ValueError):
             select(**kw)
+
+
+def test_select_runs_on_its_caches_device_and_the_calls_stream(monkeypatch):
+    """Whichever device is the current one: the library's calls are made with the
+    cache's as the current one, and on the stream that was given."""
+    import contextlib
+    import torch
+    from sparse_attention_token_idx_b200 import pipeline
+    from sparse_attention_token_idx_b200.pipeline import Indexer
+    X, at, made = pipeline.X, [(0, None)], []
+
+    @contextlib.contextmanager
+    def entered(device, stream):
+        at.append((device, stream))
+        yield
+        at.pop()
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(X, "_on", entered)
+    monkeypatch.setattr(X, "_current_device", lambda: at[-1][0])
+    monkeypatch.setattr(X, "_current_stream", lambda device: 7)
+    monkeypatch.setattr(X, "workspace_size", lambda *a: 0)
+    monkeypatch.setattr(X, "quant_queries", lambda *a, stream=None: made.append((at[-1], stream)))
+    monkeypatch.setattr(X, "score_topk_ex", lambda *a, out, ws, stream=None: made.append((at[-1], stream)))
+    ix = Indexer(2, 64, 0, 16, device="cpu")
+    ix._index = 3
+    z = torch.zeros
+    a = (z((2, 3, 64, 128), dtype=torch.bfloat16), z((2, 3, 64)), z(2, dtype=torch.int32))
+    for stream in (None, "a stream"):
+        made.clear()
+        ix.select(*a, max_len=64, stream=stream)
+        assert made == [((3, stream), None)] * 2
+    at[0] = (3, None)                                            # nothing to switch
+    made.clear()
+    ix.select(*a, max_len=64)
+    assert made == [((3, None), None)] * 2 and len(at) == 1
