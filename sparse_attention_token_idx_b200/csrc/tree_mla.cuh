@@ -258,10 +258,11 @@ struct Waits {
   }
   __device__ __forceinline__ bool nap(uint64_t* bar, uint32_t parity) const { return poll<true>(bar, parity); }
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const { return poll<false>(bar, parity); }
-  // during teardown: whatever happened before, wait (the whole warp) for what is in flight
+  // during teardown: whatever happened before, wait (the whole warp) for what is in
+  // flight; 10 ms at least, however small the budget, since memory goes back behind it
   __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
-    const uint64_t t0 = globaltimer_ns();
-    while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity) || globaltimer_ns() - t0 > budget_ns)) {}
+    const uint64_t t0 = globaltimer_ns(), limit = max(budget_ns, uint64_t{10000000});
+    while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity) || globaltimer_ns() - t0 > limit)) {}
   }
 };
 
